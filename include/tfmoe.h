@@ -319,6 +319,94 @@ TFMOE_API tfmoe_status tfmoe_route_noalloc(const uint16_t *x, int32_t T, int32_t
                                            int32_t num_experts, int32_t top_k,
                                            int32_t *ids_out, float *weights_out, void *cuda_stream);
 
+/* ------------------------------------------------------------------ the NVFP4 matrix product
+ *
+ * tfmoe_linear: one matrix product of bf16 activations with an NVFP4 weight matrix (the
+ * formats of the layer above) and its epilogue, for the projections around an MoE layer:
+ *
+ *   y[t,n]   = global * sum_k x[t,k] * E2M1(code[n,k]) * E4M3(scale[n, k/16]) + bias[n]
+ *   z[t,n]   = act(y[t,n]);  with TFMOE_ACT_SWIGLU  z[t,n] = silu(gate[t,n]) * up[t,n],
+ *              gate and up two such products (each with its own bias)
+ *   out[t,n] = round( z[t,n] + residual[t,n] )          to bf16, or fp32 (TFMOE_FLAG_OUT_FP32)
+ *
+ * The products are exact (an E2M1 value times an E4M3 value has at most 6 significant bits,
+ * a bf16 value 8), the sums, bias, activation and residual are fp32, and the result is
+ * rounded once. Two regimes, chosen by T (see tfmoe_linear_desc.flags to force one): a
+ * weight-streaming kernel for decode-sized batches and a tcgen05 kernel above.
+ */
+typedef struct tfmoe_linear tfmoe_linear;   /* opaque */
+
+typedef enum {
+    TFMOE_ACT_NONE = 0,
+    TFMOE_ACT_RELU = 1,        /* max(y, 0) */
+    TFMOE_ACT_SILU = 2,        /* y / (1 + e^-y) */
+    TFMOE_ACT_GELU = 3,        /* y (1 + erf(y / sqrt(2))) / 2 */
+    TFMOE_ACT_GELU_TANH = 4,   /* y (1 + tanh(sqrt(2/pi) (y + 0.044715 y^3))) / 2 */
+    TFMOE_ACT_SWIGLU = 5       /* silu(gate) * up: two weight matrices */
+} tfmoe_activation;
+
+#define TFMOE_FLAG_OUT_FP32      0x10u  /* tfmoe_linear: out is fp32 instead of bf16 */
+
+/*
+ * in_features K: a positive multiple of 16, at most 65536; out_features N: 1 to 2^20;
+ * max_tokens: 1 to 2^20, the largest T of a forward. flags: TFMOE_FLAG_OUT_FP32, and
+ * TFMOE_FLAG_FORCE_GEMV (the streaming regime, possible up to 16 tokens) or
+ * TFMOE_FLAG_FORCE_MMA (the tcgen05 regime at every T), which are exclusive.
+ */
+typedef struct {
+    int32_t in_features;
+    int32_t out_features;
+    int32_t max_tokens;
+    int32_t activation;        /* tfmoe_activation */
+    int32_t has_bias;          /* 1: bias is read and added */
+    uint32_t flags;            /* TFMOE_FLAG_* */
+} tfmoe_linear_desc;
+
+/* DEVICE pointers, row-major, caller-owned, read only during tfmoe_linear_load_weights. */
+typedef struct {
+    const uint8_t *codes;      /* [N][K/2]; with SWIGLU the gate matrix */
+    const uint8_t *scales;     /* e4m3 [N][K/16] */
+    const float   *global;     /* [1] */
+    const uint8_t *up_codes;   /* SWIGLU only: the up matrix, same shapes */
+    const uint8_t *up_scales;
+    const float   *up_global;
+    const float   *bias;       /* fp32 [N]; with SWIGLU [2N], gate then up; read only when has_bias */
+} tfmoe_linear_weights;
+
+/* Create a handle on the current CUDA device with its weight storage and workspace. On error
+ * *out is NULL and nothing stays allocated. */
+TFMOE_API tfmoe_status tfmoe_linear_create(const tfmoe_linear_desc *desc, tfmoe_linear **out);
+
+/* Copy and repack the weights into library-owned memory (row tiles of 128, K tiles of 64, both
+ * filled up with zeros). Synchronous, after all work enqueued on the device before it; may be
+ * called again to replace the weights. */
+TFMOE_API tfmoe_status tfmoe_linear_load_weights(tfmoe_linear *lin, const tfmoe_linear_weights *w);
+
+/*
+ * out = epilogue(x) for T rows, 0 <= T <= max_tokens (0 launches nothing). DEVICE pointers.
+ * x bf16, row t at x + t*ldx, 16-byte aligned with ldx a multiple of 8 (elements, >= K).
+ * residual bf16, row t at residual + t*ldr (ldr >= N), or NULL; out bf16 or fp32, row t at
+ * out + t*ldo (ldo >= N); both aligned to their element. Elements between the rows are neither
+ * read nor written. residual may be the same array as a bf16 out (same address and ld: the
+ * residual stream updated in place); otherwise out may not overlap x or residual (column ranges
+ * of one wider buffer with the same row stride do not overlap). Stream-ordered, never synchronises,
+ * never allocates, may be captured in a CUDA graph. One handle has one workspace: do not run
+ * two forwards of the same handle concurrently on different streams.
+ */
+TFMOE_API tfmoe_status tfmoe_linear_forward(tfmoe_linear *lin, const uint16_t *x, int64_t ldx, int32_t T,
+                                            const uint16_t *residual, int64_t ldr, void *out, int64_t ldo,
+                                            void *cuda_stream);
+
+/* Synchronise `cuda_stream`, then report a pending CUDA error or a device-side wait that gave
+ * up (and make the handle usable again). */
+TFMOE_API tfmoe_status tfmoe_linear_sync_status(tfmoe_linear *lin, void *cuda_stream);
+
+/* Number of kernel launches the last tfmoe_linear_forward enqueued. */
+TFMOE_API int32_t tfmoe_linear_last_launch_count(tfmoe_linear *lin);
+
+/* Free everything the handle owns. NULL is accepted. Synchronises the device. */
+TFMOE_API void tfmoe_linear_destroy(tfmoe_linear *lin);
+
 #ifdef __cplusplus
 }
 #endif

@@ -262,7 +262,9 @@ tfmoe_status tfmoe_load_weights(tfmoe_layer *layer, const tfmoe_weights *w)
     DeviceGuard dg(L.device);
     const size_t E = L.desc.num_experts, H = L.desc.hidden;
     cudaStream_t s;
-    cudaError_t e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+    // the caller's tensors may still be being written, and forwards may still read the old weights
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
     if (e != cudaSuccess) return cuda_fail(e, "tfmoe_load_weights: stream");
     e = cudaMemcpyAsync(L.w.router_w, w->router_w, E * H * 2, cudaMemcpyDeviceToDevice, s);
     if (e == cudaSuccess && L.desc.has_router_bias)

@@ -1,0 +1,81 @@
+// linear.h -- the handle and the launchers of the NVFP4 matrix product (tfmoe_linear_*).
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace tfmoe {
+
+// What the epilogue of one output needs. Weight rows are those of the tiled matrix: with a
+// gated activation row 2j is gate row j and row 2j+1 up row j, so N outputs have 2N rows.
+struct LinearEpilogue {
+    const float *global0, *global1;   // [1] per-tensor multipliers (gate, up when gated)
+    const float *bias;                // [N], gated [2N]; NULL = none
+    const uint16_t *residual;         // bf16 or NULL
+    int64_t ldr;
+    void *out;
+    int64_t ldo;
+    int N;
+    int act;                          // tfmoe_activation
+    int out_fp32;
+};
+
+struct Linear {
+    tfmoe_linear_desc desc{};
+    int device = 0;
+    int num_sms = 0;
+    bool loaded = false;
+    int rows = 0;                     // weight rows: N, or 2N when gated
+    int RT = 0, KT = 0;               // row tiles of 128, column tiles of 64 (zero filled)
+    void *w_block = nullptr;
+    void *ws_block = nullptr;
+    uint8_t *codes = nullptr;         // [RT][KT] tiles of kTileCodeBytes
+    uint8_t *scales = nullptr;        // [RT][KT] slabs of kTileScaleBytes
+    float *global = nullptr;          // [2]
+    float *bias = nullptr;            // [rows]
+    int32_t *err_word = nullptr;
+    int32_t last_launches = 0;
+};
+
+inline bool linear_gated(const Linear &L) { return L.desc.activation == TFMOE_ACT_SWIGLU; }
+
+cudaError_t launch_linear_repack(const Linear &L, const tfmoe_linear_weights &w, cudaStream_t s);
+cudaError_t launch_linear_simple(Linear &L, const uint16_t *x, int64_t ldx, int T, const LinearEpilogue &ep,
+                                 cudaStream_t s, int *launches);
+
+// Activations in fp32. expf, erff and the division are CUDA's own fp32 functions (a few units
+// in the last place), so an fp32 output keeps its precision.
+__device__ __forceinline__ float activate(float y, int act) {
+    switch (act) {
+    case TFMOE_ACT_RELU: return y < 0.f ? 0.f : y;            // a NaN stays a NaN
+    case TFMOE_ACT_SILU: return y / (1.0f + expf(-y));
+    case TFMOE_ACT_GELU: return 0.5f * y * (1.0f + erff(y * 0.70710678118654752f));
+    case TFMOE_ACT_GELU_TANH:
+        // (1 + tanh(z)) / 2 = 1 / (1 + e^-2z), z = sqrt(2/pi) (y + 0.044715 y^3)
+        return y / (1.0f + expf(-1.5957691216057308f * (y + 0.044715f * y * y * y)));
+    default: return y;
+    }
+}
+
+// The finished value of output n of token t from its accumulated sum(s) without multiplier.
+__device__ __forceinline__ float finish_output(const LinearEpilogue &ep, int t, int n, float s0, float s1, float g0,
+                                               float g1) {
+    float y = s0 * g0;
+    if (ep.bias) y += __ldg(ep.bias + n);
+    if (ep.act == TFMOE_ACT_SWIGLU) {
+        float u = s1 * g1;
+        if (ep.bias) u += __ldg(ep.bias + ep.N + n);
+        y = activate(y, TFMOE_ACT_SILU) * u;
+    } else {
+        y = activate(y, ep.act);
+    }
+    if (ep.residual) y += bf16_bits_to_float(ep.residual[(int64_t)t * ep.ldr + n]);
+    return y;
+}
+
+__device__ __forceinline__ void store_output(const LinearEpilogue &ep, int t, int n, float v) {
+    if (ep.out_fp32) static_cast<float *>(ep.out)[(int64_t)t * ep.ldo + n] = v;
+    else static_cast<uint16_t *>(ep.out)[(int64_t)t * ep.ldo + n] = float_to_bf16_bits_rn(v);
+}
+
+}  // namespace tfmoe

@@ -22,6 +22,9 @@ FLAG_FORCE_GEMV = 0x1
 FLAG_FORCE_MMA = 0x2
 FLAG_DEBUG_CHECKS = 0x4
 FLAG_TEST_TIMEOUT = 0x8
+FLAG_OUT_FP32 = 0x10       # Linear only
+
+ACTIVATIONS = ["none", "relu", "silu", "gelu", "gelu_tanh", "swiglu"]   # tfmoe_activation, in order
 
 BUF_LOGITS, BUF_TOPK_IDS, BUF_TOPK_WEIGHTS, BUF_EXPERT_COUNTS, BUF_EXPERT_OFFSETS, BUF_PERM, BUF_INV, \
     BUF_ACT, BUF_EXPERT_OUT, BUF_REGIME = range(10)
@@ -29,7 +32,8 @@ BUF_LOGITS, BUF_TOPK_IDS, BUF_TOPK_WEIGHTS, BUF_EXPERT_COUNTS, BUF_EXPERT_OFFSET
 EXPORTED = ["tfmoe_create", "tfmoe_load_weights", "tfmoe_forward", "tfmoe_forward_host", "tfmoe_sync_status",
             "tfmoe_destroy", "tfmoe_last_error", "tfmoe_get_buffer", "tfmoe_last_launch_count",
             "tfmoe_profile_enable", "tfmoe_profile_read", "tfmoe_route_noalloc", "tfmoe_forward_stage",
-            "tfmoe_forward_add_norm"]
+            "tfmoe_forward_add_norm", "tfmoe_linear_create", "tfmoe_linear_load_weights", "tfmoe_linear_forward",
+            "tfmoe_linear_sync_status", "tfmoe_linear_last_launch_count", "tfmoe_linear_destroy"]
 
 ROUTE_NOALLOC_MAX_LOGITS = 1 << 20
 
@@ -52,6 +56,16 @@ class Weights(ctypes.Structure):
         "shared_gate_codes", "shared_up_codes", "shared_gate_scales", "shared_up_scales",
         "shared_gate_global", "shared_up_global", "shared_down_codes", "shared_down_scales",
         "shared_down_global")]
+
+
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("max_tokens", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("has_bias", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class LinearWeights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "codes", "scales", "global", "up_codes", "up_scales", "up_global", "bias")]
 
 
 class TfmoeError(RuntimeError):
@@ -100,6 +114,19 @@ def load_library(path: str = LIB_PATH):
     lib.tfmoe_forward_stage.restype = ctypes.c_int
     lib.tfmoe_route_noalloc.argtypes = [vp, i32, i32, vp, vp, i32, i32, vp, vp, vp]
     lib.tfmoe_route_noalloc.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    lib.tfmoe_linear_create.argtypes = [ctypes.POINTER(LinearDesc), ctypes.POINTER(vp)]
+    lib.tfmoe_linear_create.restype = ctypes.c_int
+    lib.tfmoe_linear_load_weights.argtypes = [vp, ctypes.POINTER(LinearWeights)]
+    lib.tfmoe_linear_load_weights.restype = ctypes.c_int
+    lib.tfmoe_linear_forward.argtypes = [vp, vp, i64, i32, vp, i64, vp, i64, vp]
+    lib.tfmoe_linear_forward.restype = ctypes.c_int
+    lib.tfmoe_linear_sync_status.argtypes = [vp, vp]
+    lib.tfmoe_linear_sync_status.restype = ctypes.c_int
+    lib.tfmoe_linear_last_launch_count.argtypes = [vp]
+    lib.tfmoe_linear_last_launch_count.restype = i32
+    lib.tfmoe_linear_destroy.argtypes = [vp]
+    lib.tfmoe_linear_destroy.restype = None
     del u32
     _lib = lib
     return lib
@@ -222,6 +249,83 @@ class MoELayer:
     def close(self):
         if getattr(self, "handle", None) is not None and self.handle.value:
             self.lib.tfmoe_destroy(self.handle)
+            self.handle = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _rows(t, name: str, width: int, dtypes, rows: Optional[int], device):
+    """(pointer, row stride in elements) of a 2-D tensor whose rows are contiguous runs of `width`."""
+    if t.dim() != 2 or t.shape[1] != width or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must be [{'T' if rows is None else rows}, {width}], got {list(t.shape)}")
+    if str(t.dtype).replace("torch.", "") not in dtypes:
+        raise TypeError(f"{name} must be {dtypes[0]}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows, got strides {t.stride()}")
+    # the stride of a single row is arbitrary and never used
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else (width + 7) // 8 * 8)
+
+
+_BF16 = ("bfloat16", "int16", "uint16")   # bf16, or its raw bits
+
+
+class Linear:
+    """One NVFP4 W4A16 matrix product with bias, activation and residual (tfmoe_linear_*), held by
+    libtfmoe on the current CUDA device. activation: one of ACTIVATIONS."""
+
+    def __init__(self, in_features: int, out_features: int, max_tokens: int, activation: str = "none",
+                 has_bias: bool = False, out_fp32: bool = False, flags: int = 0):
+        import torch
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"activation must be one of {ACTIVATIONS}, got {activation!r}")
+        self.lib = load_library()
+        self.desc = LinearDesc(in_features, out_features, max_tokens, ACTIVATIONS.index(activation),
+                               1 if has_bias else 0, flags | (FLAG_OUT_FP32 if out_fp32 else 0))
+        h = ctypes.c_void_p()
+        check(self.lib.tfmoe_linear_create(ctypes.byref(self.desc), ctypes.byref(h)))
+        self.handle = h
+        self.device = torch.device("cuda", torch.cuda.current_device())
+        fp32 = bool(self.desc.flags & FLAG_OUT_FP32)
+        self._out_dtype = torch.float32 if fp32 else torch.bfloat16
+        self._out_names = ("float32",) if fp32 else _BF16
+
+    def load_weights(self, w: Dict[str, "object"]):
+        """w: device tensors "codes", "scales", "global", with swiglu also "up_codes", "up_scales" and
+        "up_global", and "bias" (layouts of tfmoe_linear_weights)."""
+        ws = LinearWeights(*[_ptr(w.get(n)) for n, _ in LinearWeights._fields_])
+        check(self.lib.tfmoe_linear_load_weights(self.handle, ctypes.byref(ws)))
+
+    def forward(self, x, residual=None, out=None, stream=None):
+        """x [T, in_features] bf16 (rows may be a slice of wider ones); residual and out [T, out_features]
+        likewise, out may be a bf16 residual itself. Returns out."""
+        import torch
+        K, N = self.desc.in_features, self.desc.out_features
+        xp, ldx = _rows(x, "x", K, _BF16, None, self.device)
+        T = x.shape[0]
+        if out is None:
+            out = torch.empty((T, N), dtype=self._out_dtype, device=self.device)
+        op, ldo = _rows(out, "out", N, self._out_names, T, self.device)
+        rp, ldr = (None, 0) if residual is None else _rows(residual, "residual", N, _BF16, T, self.device)
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        check(self.lib.tfmoe_linear_forward(self.handle, xp, ldx, T, rp, ldr, op, ldo, stream.cuda_stream))
+        return out
+
+    def sync_status(self, stream=None) -> int:
+        return self.lib.tfmoe_linear_sync_status(self.handle, _stream_handle(stream))
+
+    def last_launch_count(self) -> int:
+        return int(self.lib.tfmoe_linear_last_launch_count(self.handle))
+
+    def close(self):
+        if getattr(self, "handle", None) is not None and self.handle.value:
+            self.lib.tfmoe_linear_destroy(self.handle)
             self.handle = ctypes.c_void_p()
 
     def __del__(self):
