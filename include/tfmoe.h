@@ -350,7 +350,7 @@ typedef enum {
 /*
  * in_features K: a positive multiple of 16, at most 65536; out_features N: 1 to 2^20;
  * max_tokens: 1 to 2^20, the largest T of a forward. flags: TFMOE_FLAG_OUT_FP32, and
- * TFMOE_FLAG_FORCE_GEMV (the streaming regime, possible up to 16 tokens) or
+ * TFMOE_FLAG_FORCE_GEMV (the streaming regime: up to 16 tokens, T * K up to about 64000) or
  * TFMOE_FLAG_FORCE_MMA (the tcgen05 regime at every T), which are exclusive.
  */
 typedef struct {

@@ -188,20 +188,24 @@ tfmoe_status tfmoe_linear_create(const tfmoe_linear_desc *desc, tfmoe_linear **o
     const size_t tiles = (size_t)L.RT * L.KT;
     const size_t small = 256 + (((size_t)L.rows * 4 + 255) & ~(size_t)255);      // global, bias
     e = cudaMalloc(&L.w_block, tiles * (kTileCodeBytes + kTileScaleBytes) + small);
-    if (e == cudaSuccess) e = cudaMalloc(&L.ws_block, 256);
-    if (e == cudaSuccess) e = cudaMemset(L.ws_block, 0, 256);
+    L.zero_bytes = (256 + (size_t)L.RT * 4 + 255) & ~(size_t)255;
+    if (e == cudaSuccess) e = cudaMalloc(&L.ws_block, L.zero_bytes + linear_stream_partial_floats(L) * 4);
+    if (e == cudaSuccess) e = cudaMemset(L.ws_block, 0, L.zero_bytes);
+    if (e == cudaSuccess) e = linear_stream_setup(L);
     if (e != cudaSuccess) {
         cudaGetLastError();
         if (L.w_block) cudaFree(L.w_block);
         if (L.ws_block) cudaFree(L.ws_block);
         delete h;
-        return cuda_fail(e, "tfmoe_linear_create: cudaMalloc");
+        return cuda_fail(e, "tfmoe_linear_create");
     }
     L.codes = static_cast<uint8_t *>(L.w_block);
     L.scales = L.codes + tiles * kTileCodeBytes;
     L.global = reinterpret_cast<float *>(L.scales + tiles * kTileScaleBytes);
     L.bias = L.global + 64;
     L.err_word = static_cast<int32_t *>(L.ws_block);
+    L.tickets = L.err_word + 64;
+    L.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(L.ws_block) + L.zero_bytes);
     *out = h;
     return record_ok();
 }
@@ -261,8 +265,9 @@ tfmoe_status tfmoe_linear_forward(tfmoe_linear *lin, const uint16_t *x, int64_t 
                             (long long)ldx);
     if ((reinterpret_cast<uintptr_t>(residual) & 1u) || (reinterpret_cast<uintptr_t>(out) & (f32 ? 3u : 1u)))
         return record_error(TFMOE_ERR_INVALID_ARG, "%s: residual and out must be aligned to their element", who);
-    if ((L.desc.flags & TFMOE_FLAG_FORCE_GEMV) && T > 16)
-        return record_error(TFMOE_ERR_UNSUPPORTED, "%s: FORCE_GEMV takes at most 16 tokens (T=%d)", who, T);
+    if ((L.desc.flags & TFMOE_FLAG_FORCE_GEMV) && !linear_stream_fits(L, T))
+        return record_error(TFMOE_ERR_UNSUPPORTED, "%s: the streaming regime takes at most 16 tokens whose rows fit in "
+                            "shared memory (T=%d, K=%d)", who, T, K);
     const uint64_t es = f32 ? 4 : 2;
     const Rows rx{reinterpret_cast<uintptr_t>(x), (uint64_t)K * 2, (uint64_t)ldx * 2, T};
     const Rows ro{reinterpret_cast<uintptr_t>(out), (uint64_t)N * es, (uint64_t)ldo * es, T};
@@ -285,7 +290,10 @@ tfmoe_status tfmoe_linear_forward(tfmoe_linear *lin, const uint16_t *x, int64_t 
     ep.act = L.desc.activation;
     ep.out_fp32 = f32;
     int n = 0;
-    const cudaError_t e = launch_linear_simple(L, x, ldx, T, ep, static_cast<cudaStream_t>(cuda_stream), &n);
+    const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    const cudaError_t e = linear_stream_fits(L, T) && !(L.desc.flags & TFMOE_FLAG_FORCE_MMA)
+                              ? launch_linear_stream(L, x, ldx, T, ep, s, &n)
+                              : launch_linear_simple(L, x, ldx, T, ep, s, &n);
     L.last_launches = n;
     if (e != cudaSuccess) return cuda_fail(e, who);
     return record_ok();
@@ -301,7 +309,7 @@ tfmoe_status tfmoe_linear_sync_status(tfmoe_linear *lin, void *cuda_stream)
     if (e != cudaSuccess) return cuda_fail(e, "tfmoe_linear_sync_status");
     int32_t word = 0;
     e = cudaMemcpy(&word, L.err_word, sizeof word, cudaMemcpyDeviceToHost);
-    if (e == cudaSuccess && word != 0) e = cudaMemset(L.ws_block, 0, 256);
+    if (e == cudaSuccess && word != 0) e = cudaMemset(L.ws_block, 0, L.zero_bytes);
     if (e != cudaSuccess) return cuda_fail(e, "tfmoe_linear_sync_status: error word");
     if (word) return record_error(TFMOE_ERR_TIMEOUT, "a device-side wait timed out (word 0x%x)", word);
     return record_ok();
