@@ -8,21 +8,22 @@
 // inside one row tile is a piece; a row tile cut by a CTA border has its pieces' sums added
 // afterwards in CTA order, so equal calls give equal bits.
 //
-// One producer lane fills a ring of slots with bulk copies; a slot holds a group of one or two
-// consecutive units of a piece. 16 consumer warps: warp w takes 16 rows (w mod 8) of the groups
-// whose running number has the parity w / 8. The product runs on mma.sync m16n8k16 (f16 in, fp32
+// One producer lane fills a ring of slots with bulk copies; a slot holds the units of a piece whose
+// column tiles lie in one aligned window of four (two copies: a bulk copy costs the issuing
+// lane about 100 clocks, so small ones would set the pace). 16 consumer warps: warp w takes 16 rows
+// (w mod 8) of pair w / 8 of every window. The product runs on mma.sync m16n8k16 (f16 in, fp32
 // sums), rows of weights against up to 8 tokens per instruction: the tensor core is idle most of
 // the time either way, and this form needs no tensor memory round trip for a few tokens. What has
 // to keep up with HBM (23 bytes = 41 weights per clock and SM) is the decode, one conversion
-// and one scale multiplication per two weights; on CUDA cores the products would add an FMA per
-// weight and token.
+// and one scale multiplication per two weights: measured alone, two units take 272 clocks of an SM
+// (8 tokens) or 405 (16 tokens) against 400 at HBM speed. On CUDA cores the products would add an
+// FMA per weight and token.
 //
 // The order of the reduction is free, so the lanes read what they can use: lane (g, t) = (l / 4,
-// l % 4) owns rows g and g + 8 and the t-th 32-column half of the group: one 16-byte load per row,
-// and chunk i (8 columns) of every lane's half forms the k indices of two instructions. The
-// halves are copied 32 bytes apart from a multiple of 128 (and the second unit's scales
-// likewise), which spreads the four lanes of a row over the banks. Token operands are stored
-// in that order too: [128 columns][chunk 0..3][half 0..3][8 values].
+// l % 4) owns rows g and g + 8 and the t-th 32-column half of the pair, four chunks of 8 columns (one
+// word of codes each) in the order t, t + 1, t + 2, t + 3 (mod 4), which puts the 32 lanes on
+// different banks. Chunk i of every lane forms the k indices of two instructions. Token operands
+// are stored in that order too: [128 columns][step 0..3][half 0..3][8 values].
 #pragma once
 
 #include "common.cuh"
@@ -34,12 +35,11 @@ namespace stream {
 constexpr int kConsumers = 16;                           // warps
 constexpr int kConsumerThreads = 32 * kConsumers;
 constexpr int kThreads = kConsumerThreads + 32;          // + the producer warp
-constexpr int kHalfStride = kTileCodeBytes / 2 + 32;     // 2080
-constexpr int kScaleAt = 4 * kHalfStride;                // 8320
-constexpr int kScaleStride = kTileScaleBytes + 32;       // 544
-constexpr int kSlotBytes = kScaleAt + kScaleStride + kTileScaleBytes;   // 9376
-static_assert(kSlotBytes % 16 == 0, "bulk copies need 16-byte aligned slots");
-constexpr int kMaxSlots = 24;
+constexpr int kWindow = 4;                               // column tiles per slot
+constexpr int kScaleAt = kWindow * kTileCodeBytes;       // 16384
+constexpr int kSlotBytes = kScaleAt + kWindow * kTileScaleBytes;   // 18432
+static_assert(kSlotBytes % 128 == 0, "bulk copies need 16-byte aligned slots");
+constexpr int kMaxSlots = 12;
 constexpr int kMaxTokens = 16;                           // two n = 8 tiles
 
 // Shared-memory bytes of one token's operand row for K = 64 KT columns. The 64 bytes at the
@@ -47,7 +47,7 @@ constexpr int kMaxTokens = 16;                           // two n = 8 tiles
 __host__ __device__ constexpr uint32_t row_bytes(int KT) { return (uint32_t)((KT + 1) / 2) * 256u + 64u; }
 // Byte offset of the 8-value chunk holding column k (a multiple of 8) inside its row.
 __host__ __device__ constexpr uint32_t chunk_offset(int k) {
-    return (uint32_t)(k >> 7) * 256u + (uint32_t)((k >> 3) & 3) * 64u + (uint32_t)((k >> 5) & 3) * 16u;
+    return (uint32_t)(k >> 7) * 256u + (uint32_t)(((k >> 3) - (k >> 5)) & 3) * 64u + (uint32_t)((k >> 5) & 3) * 16u;
 }
 
 // First unit of CTA c, and the CTA that owns unit u, when U units are cut into G runs.
@@ -88,7 +88,7 @@ struct Cursor {
     uint32_t phase = 0;
     __device__ __forceinline__ void advance(int by, int n) {
         slot += by;
-        while (slot >= n) { slot -= n; phase ^= 1u; }
+        if (slot >= n) { slot -= n; phase ^= 1u; }
     }
 };
 
@@ -97,25 +97,21 @@ __device__ __forceinline__ void bulk_at(uint32_t dst, const void *src, uint32_t 
                  ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
-// The producer's side: put one piece (units consecutive units from `codes` / `scales`) into the
-// ring. `issued` counts the groups. Returns false after an abort.
+// The producer's side: put the column tiles [ka, kb) of one row tile into the ring, whose codes
+// and scales start at `codes` and `scales` (those of column tile 0). Returns false after an abort.
 __device__ __forceinline__ bool produce_piece(const Ring &r, Cursor &c, uint32_t &issued, const uint8_t *codes,
-                                              const uint8_t *scales, int units) {
-    for (int u = 0; u < units; u += 2) {
-        const int n = min(2, units - u);
+                                              const uint8_t *scales, int ka, int kb) {
+    for (int k = ka; k < kb;) {
+        const int at = k % kWindow, n = min(kWindow - at, kb - k);
         const uint32_t full = r.full + 8u * c.slot, slot = r.slots + (uint32_t)c.slot * kSlotBytes;
         if (issued >= (uint32_t)r.n && !wait(r, r.empty + 8u * c.slot, c.phase ^ 1u)) return false;
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
                      ::"r"(full), "r"((uint32_t)n * (kTileCodeBytes + kTileScaleBytes)) : "memory");
-        for (int i = 0; i < n; ++i) {
-            const uint8_t *cp = codes + (size_t)(u + i) * kTileCodeBytes;
-            bulk_at(slot + (2 * i) * kHalfStride, cp, kTileCodeBytes / 2, full);
-            bulk_at(slot + (2 * i + 1) * kHalfStride, cp + kTileCodeBytes / 2, kTileCodeBytes / 2, full);
-            bulk_at(slot + kScaleAt + i * kScaleStride, scales + (size_t)(u + i) * kTileScaleBytes, kTileScaleBytes,
-                    full);
-        }
+        bulk_at(slot + at * kTileCodeBytes, codes + (size_t)k * kTileCodeBytes, n * kTileCodeBytes, full);
+        bulk_at(slot + kScaleAt + at * kTileScaleBytes, scales + (size_t)k * kTileScaleBytes, n * kTileScaleBytes, full);
         c.advance(1, r.n);
         ++issued;
+        k += n;
     }
     return true;
 }
@@ -136,6 +132,11 @@ __device__ __forceinline__ void drain(const Ring &r, const Cursor &end, uint32_t
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
 }
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
@@ -171,66 +172,130 @@ struct Acc {
     __device__ __forceinline__ float sum(int n, int j) const { return c[0][n][j] + c[1][n][j]; }
 };
 
-// One group: `units` (1 or 2) units whose first column tile is kt. xa: the lane's token row per
-// n-tile (token 8 n + g; any valid row where there is no such token). Products E2M1 * E4M3 are
-// exact in f16 (at most 6 significant bits, 2^-10 to 2688).
+// What a consumer lane needs of its place, computed once.
+struct Lane {
+    uint32_t code[4];      // offsets of the lane's four words of row g inside a window's pair, step by step
+    uint32_t scale;        // offset of row g's two scale bytes
+    uint32_t sel[2];       // prmt selectors: (scale of step 0, of step 2), (of step 1, of step 3)
+    uint32_t x;            // offset inside 128 columns of a token row
+    int unit;              // the lane's unit of a window
+    __device__ __forceinline__ Lane() {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const int row = (warp & 7) * 16 + g;
+        unit = 2 * (warp >> 3) + (t >> 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            code[i] = (uint32_t)(unit * kTileCodeBytes + (t & 1) * (kTileCodeBytes / 2) + row * 16 + ((i + t) & 3) * 4);
+        scale = (uint32_t)(kScaleAt + unit * kTileScaleBytes + row * 4 + (t & 1) * 2);
+        sel[0] = (t >> 1) ? 0x1032u : 0x3210u;               // steps 0 and 2 are in different 16-column blocks,
+        sel[1] = (((1 + t) & 3) >> 1) ? 0x1032u : 0x3210u;   // and so are steps 1 and 3
+        x = (uint32_t)(warp >> 3) * 256u + (uint32_t)t * 16u;
+    }
+};
+
+// The codes and scales of the lane's rows of one pair, in registers.
+struct Pair {
+    uint32_t w0[4], w1[4], s0, s1;
+    __device__ __forceinline__ void load(uint32_t slot, const Lane &ln) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w0[i] = lds32(slot + ln.code[i]);
+            w1[i] = lds32(slot + ln.code[i] + 128u);
+        }
+        s0 = lds16(slot + ln.scale);
+        s1 = lds16(slot + ln.scale + 32u);
+    }
+};
+
+// One pair of a window. x: the lane's operands (token 8 n + g; any valid row where there is no such
+// token) at the pair's columns. Products E2M1 * E4M3 are exact in f16 (at most 6 significant
+// bits, 2^-10 to 2688).
 template <int NT>
-__device__ __forceinline__ void consume_group(uint32_t slot, int units, int kt, int rows16, const uint32_t (&xa)[NT],
-                                              uint32_t zeros, Acc<NT> &acc) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const bool live = (t >> 1) < units;
-    const uint32_t code = slot + (uint32_t)t * kHalfStride + (uint32_t)(rows16 + g) * 16u;
-    const uint32_t scale = slot + kScaleAt + (uint32_t)(t >> 1) * kScaleStride + (uint32_t)(rows16 + g) * 4u + (t & 1) * 2u;
-    const int kl = kt + (t >> 1);
-    const uint32_t xo = (uint32_t)(kl >> 1) * 256u + (uint32_t)((kl & 1) * 2 + (t & 1)) * 16u;
-    const uint4 c0 = lds128(code), c1 = lds128(code + 128);
-    // a lane without a unit multiplies zeros by zero scales (zero times what an earlier group or an
-    // infinite activation left there could be a NaN)
-    const uint32_t s0 = live ? lds16(scale) : 0u, s1 = live ? lds16(scale + 32) : 0u;
-    const uint32_t h0 = e4m3x2_to_f16x2(s0), h1 = e4m3x2_to_f16x2(s1);
-    const __half2 v0 = *reinterpret_cast<const __half2 *>(&h0), v1 = *reinterpret_cast<const __half2 *>(&h1);
-    const __half2 sc0[2] = {__low2half2(v0), __high2half2(v0)}, sc1[2] = {__low2half2(v1), __high2half2(v1)};
-    const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
+__device__ __forceinline__ void consume_pair(const Pair &p, const Lane &ln, const uint32_t (&x)[NT], Acc<NT> &acc) {
+    const uint32_t h0 = e4m3x2_to_f16x2(p.s0), h1 = e4m3x2_to_f16x2(p.s1);
+    __half2 v0[2], v1[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t a = __byte_perm(h0, 0, ln.sel[j]), b = __byte_perm(h1, 0, ln.sel[j]);
+        v0[j] = *reinterpret_cast<const __half2 *>(&a);
+        v1[j] = *reinterpret_cast<const __half2 *>(&b);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t a[4], b[4];
-        e2m1x8_to_f16x2x4(w0[i], a);
-        e2m1x8_to_f16x2x4(w1[i], b);
+        e2m1x8_to_f16x2x4(p.w0[i], a);
+        e2m1x8_to_f16x2x4(p.w1[i], b);
+        const __half2 sa = i < 2 ? __low2half2(v0[i & 1]) : __high2half2(v0[i & 1]);
+        const __half2 sb = i < 2 ? __low2half2(v1[i & 1]) : __high2half2(v1[i & 1]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            a[j] = mul_f16x2(a[j], sc0[i >> 1]);
-            b[j] = mul_f16x2(b[j], sc1[i >> 1]);
+            a[j] = mul_f16x2(a[j], sa);
+            b[j] = mul_f16x2(b[j], sb);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const uint4 x = lds128((live ? xa[n] + xo : zeros) + 64u * i);
-            mma_f16(acc.c[0][n], a[0], b[0], a[1], b[1], x.x, x.y);
-            mma_f16(acc.c[1][n], a[2], b[2], a[3], b[3], x.z, x.w);
+            const uint4 xv = lds128(x[n] + 64u * i);
+            mma_f16(acc.c[0][n], a[0], b[0], a[1], b[1], xv.x, xv.y);
+            mma_f16(acc.c[1][n], a[2], b[2], a[3], b[3], xv.z, xv.w);
         }
     }
 }
 
-// One piece: this warp's share of its groups. `c` is at the piece's first group, whose running
-// number has parity `par0`.
+// One piece, the column tiles [ka, kb) of a row tile: this warp's share of its windows. xa: the
+// lane's token rows. Whole windows run two at a time: the next one's codes are read (and its slot
+// handed back) before the current one is multiplied.
 template <int NT>
-__device__ __forceinline__ void consume_piece(const Ring &r, Cursor &c, uint32_t &par0, int kt, int units,
+__device__ __forceinline__ void consume_piece(const Ring &r, Cursor &c, const Lane &ln, int ka, int kb,
                                               const uint32_t (&xa)[NT], Acc<NT> &acc) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rows16 = (warp & 7) * 16;
-    const int groups = (units + 1) / 2;
-    int first = (int)((uint32_t)(warp >> 3) ^ par0);       // 0 or 1: the warp's first group
-    Cursor my = c;
-    if (first) my.advance(1, r.n);
-    for (int gi = first; gi < groups; gi += 2) {
-        wait(r, r.full + 8u * my.slot, my.phase);
+    const int lane = threadIdx.x & 31;
+    int w = ka & ~(kWindow - 1);
+    uint32_t x[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) x[n] = xa[n] + ln.x + (uint32_t)w * 128u;
+    auto step = [&]() {
+        w += kWindow;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[n] += kWindow * 128u;
+    };
+    auto fetch = [&](Pair &p) {
+        wait(r, r.full + 8u * c.slot, c.phase);
+        p.load(r.slots + (uint32_t)c.slot * kSlotBytes, ln);
         __syncwarp();
-        consume_group<NT>(r.slots + (uint32_t)my.slot * kSlotBytes, min(2, units - 2 * gi), kt + 2 * gi, rows16, xa,
-                          r.zeros, acc);
-        __syncwarp();
-        if (lane == 0) mbar_arrive_at(r.empty + 8u * my.slot);
-        my.advance(2, r.n);
+        if (lane == 0) mbar_arrive_at(r.empty + 8u * c.slot);
+        c.advance(1, r.n);
+    };
+    // a window of which the piece has only some units: a lane without a unit multiplies zeros by zero
+    // scales (zero times what an earlier window or an infinite activation left there could be a NaN)
+    auto part = [&]() {
+        Pair p;
+        fetch(p);
+        const bool live = w + ln.unit >= ka && w + ln.unit < kb;
+        if (!live) p.s0 = p.s1 = 0u;
+        uint32_t xl[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) xl[n] = live ? x[n] : r.zeros;
+        if (__any_sync(0xffffffffu, live)) consume_pair<NT>(p, ln, xl, acc);
+        step();
+    };
+    if (w < ka || w + kWindow > kb) part();
+    int whole = (kb - w) / kWindow;
+    if (whole > 0) {
+        Pair p0, p1;
+        fetch(p0);
+        for (; whole >= 2; whole -= 2) {
+            fetch(p1);
+            consume_pair<NT>(p0, ln, x, acc);
+            step();
+            if (whole > 2) fetch(p0);
+            consume_pair<NT>(p1, ln, x, acc);
+            step();
+        }
+        if (whole) {
+            consume_pair<NT>(p0, ln, x, acc);
+            step();
+        }
     }
-    c.advance(groups, r.n);
-    par0 ^= (uint32_t)groups & 1u;
+    if (w < kb) part();
 }
 
 // Barrier among the consumer warps.
@@ -271,17 +336,66 @@ __device__ __forceinline__ uint4 bf16x8_to_f16(const uint4 &v, float up) {
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
-__device__ __forceinline__ uint32_t max_exponent(const uint4 &v) {
+// Largest magnitude bits of eight bf16 values, in both halves of a word (not yet joined).
+__device__ __forceinline__ uint32_t max_bits(const uint4 &v, uint32_t m) {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-    uint32_t e = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) e = max(e, max((u[j] >> 7) & 0xFFu, (u[j] >> 23) & 0xFFu));
-    return e;
+    for (int j = 0; j < 4; ++j) asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(u[j] & 0x7FFF7FFFu));
+    return m;
 }
 // The power of two that brings a row whose largest exponent field is emax just below 2^15, as the
 // exponent field of its float; the inverse's field is 254 minus it.
 __device__ __forceinline__ int up_field(uint32_t emax) {
     return 127 + max(-120, min(120, 14 - ((int)emax - 127)));
+}
+__device__ __forceinline__ float up_of(uint32_t emax) { return __uint_as_float((uint32_t)up_field(emax) << 23); }
+__device__ __forceinline__ float inverse_up(uint32_t emax) {
+    return __uint_as_float((uint32_t)(254 - up_field(emax)) << 23);
+}
+
+// Turn T bf16 rows of K values that lie in shared memory (row_bytes(KT) apart) into operand rows in
+// place, by all consumers: the 128-column groups for which used(group) holds become f16 times a power
+// of two per row (exact for every element within 2^28 of the row's largest used one; smaller ones
+// are rounded to 2^-39 of it), with columns from K on zero. emax[t] (zero before) receives the
+// rows' largest exponent fields. Ends with a consumer barrier.
+template <class Used>
+__device__ __forceinline__ void convert_rows(uint8_t *rows, int T, int K, int KT, uint32_t *emax, Used used) {
+    const int chunks = ((KT + 1) / 2) * 16;
+    int tpr = kConsumerThreads;                              // threads per row, at least a warp
+    while (tpr * T > kConsumerThreads) tpr >>= 1;
+    const int t = threadIdx.x / tpr, i0 = threadIdx.x % tpr;
+    uint8_t *row = rows + t * row_bytes(KT);
+    if (t < T) {
+        uint32_t m = 0;
+#pragma unroll 4
+        for (int i = i0; i < chunks; i += tpr)
+            if (i * 8 < K && used(i >> 4)) m = max_bits(*reinterpret_cast<const uint4 *>(row + 16 * i), m);
+        const uint32_t e = __reduce_max_sync(0xffffffffu, max(m >> 23, (m >> 7) & 0xFFu));
+        if ((threadIdx.x & 31) == 0) atomicMax(&emax[t], e);
+    }
+    consumer_sync();
+    if (t < T) {
+        // a half warp turns groups of 16 chunks, each read by its lanes before any writes it
+        const float up = up_of(emax[t]);
+        const uint32_t half = 0xFFFFu << (threadIdx.x & 16);
+        for (int i = i0; i < chunks; i += 4 * tpr) {         // chunks and tpr are multiples of 16
+            uint4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int ij = i + j * tpr;
+                v[j] = make_uint4(0, 0, 0, 0);
+                if (ij * 8 < K && used(ij >> 4)) v[j] = *reinterpret_cast<const uint4 *>(row + 16 * ij);
+            }
+            __syncwarp(half);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int ij = i + j * tpr;
+                if (ij < chunks && used(ij >> 4))
+                    *reinterpret_cast<uint4 *>(row + chunk_offset(ij * 8)) = bf16x8_to_f16(v[j], up);
+            }
+        }
+    }
+    consumer_sync();
 }
 
 }  // namespace stream
