@@ -39,7 +39,7 @@ struct Layout {
         zeros = sums + kMaxTokens * kSumStride * 4;
         emax = zeros + 256;
         bars = emax + kMaxTokens * 4;
-        total = bars + (2 * kMaxSlots + 2) * 8;          // full, empty, token rows landed, abort flag
+        total = bars + (2 * kMaxSlots + 2) * 8;          // full, empty, rows requested, abort flag
     }
 };
 
@@ -61,7 +61,7 @@ template <int NT>
 __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const StreamArgs a)
 {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int last[2];
+    __shared__ int join[2][3];                              // per cut piece: last to arrive, first and last CTA of the tile
     const Layout lay(a.T, a.KT, a.slots);
     float *sums = reinterpret_cast<float *>(smem + lay.sums);
     uint32_t *emax = reinterpret_cast<uint32_t *>(smem + lay.emax);
@@ -74,75 +74,53 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
     ring.zeros = smem_u32(smem + lay.zeros);
     ring.n = a.slots;
     ring.abort_flag = reinterpret_cast<volatile int32_t *>(bars + 2 * kMaxSlots + 1);
+    const uint32_t requested = ring.full + 8u * (2 * kMaxSlots);
     ring.err_word = a.err_word;
-    const uint32_t xfull = ring.full + 8u * (2 * kMaxSlots);
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < a.slots; ++i) {
-            mbar_init(bars + i, 1);
-            mbar_init(bars + kMaxSlots + i, kConsumers);
-        }
-        mbar_init(bars + 2 * kMaxSlots, 1);
-        *ring.abort_flag = 0;
-        fence_mbar_init();
-    }
-    if (threadIdx.x < kMaxTokens) emax[threadIdx.x] = 0;
-    if (threadIdx.x < 64) reinterpret_cast<uint32_t *>(smem + lay.zeros)[threadIdx.x] = 0;
-    __syncthreads();
-    grid_dep_launch_dependents();
-
     const uint32_t G = gridDim.x, c = blockIdx.x, U = (uint32_t)a.RT * a.KT;
     const uint32_t u0 = first_unit(c, U, G), u1 = first_unit(c + 1, U, G);
-    const int q0 = (int)(u0 / a.KT), k0 = (int)(u0 % a.KT);           // u0 < u1: G <= U
-    const int q1 = (int)((u1 - 1) / a.KT), k1 = (int)((u1 - 1) % a.KT) + 1;
-    // the columns this CTA uses: [xa0, xb0) and, when its run wraps into the next row tile, [0, xb1)
-    const bool all = q1 > q0 + 1 || (q1 == q0 + 1 && k1 >= (k0 & ~1));
-    const int xa0 = all ? 0 : (k0 & ~1) * kTileK, xb0 = min(a.K, (q1 > q0 ? a.KT : (k1 + 1) & ~1) * kTileK);
-    const int xb1 = all || q1 == q0 ? 0 : min(xa0, ((k1 + 1) & ~1) * kTileK);
+    const int q0 = (int)(u0 / a.KT), k0 = (int)(u0 - (uint32_t)q0 * a.KT);                   // u0 < u1: G <= U
+    const int q1 = (int)((u1 - 1) / a.KT), k1 = (int)(u1 - 1 - (uint32_t)q1 * a.KT) + 1;
+    grid_dep_launch_dependents();
     if (warp == kConsumers) {
+        if (lane < a.slots) {
+            mbar_init(bars + lane, 1);
+            mbar_init(bars + kMaxSlots + lane, kConsumers);
+        }
+        if (lane == 0) {
+            mbar_init(bars + 2 * kMaxSlots, kConsumers);
+            *ring.abort_flag = 0;
+        }
+        fence_mbar_init();
+        __syncwarp();
+        asm volatile("bar.arrive 2, %0;" ::"n"(kThreads) : "memory");   // the consumers wait there
         if (lane == 0) {
             Cursor cur;
             uint32_t issued = 0;
-            // One slot of weights, which no kernel writes, then the rows, then the rest: rows behind a
-            // full ring would wait for 150 KB of weights.
-            bool ok = true, rows = false;
-            for (int q = q0; q <= q1 && ok; ++q) {
-                const int ka = q == q0 ? k0 : 0, kb = q == q1 ? k1 : a.KT;
-                const uint8_t *codes = a.codes + (size_t)q * a.KT * kTileCodeBytes;
-                const uint8_t *scales = a.scales + (size_t)q * a.KT * kTileScaleBytes;
-                int k = ka;
-                if (!rows) {
-                    k = min(kb, (ka & ~(kWindow - 1)) + kWindow);
-                    ok = produce_piece(ring, cur, issued, codes, scales, ka, k);
-                    rows = true;
-                    grid_dep_wait();
-                    const uint32_t bytes = (uint32_t)(xb0 - xa0 + xb1) * 2u;
-                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
-                                 ::"r"(xfull), "r"(bytes * a.T) : "memory");
-                    for (int t = 0; t < a.T; ++t) {
-                        const uint32_t dst = ring.slots + lay.x + t * row_bytes(a.KT);
-                        const uint16_t *src = a.x + (int64_t)t * a.ldx;
-                        bulk_at(dst + xa0 * 2, src + xa0, (uint32_t)(xb0 - xa0) * 2u, xfull);
-                        if (xb1) bulk_at(dst, src, (uint32_t)xb1 * 2u, xfull);
-                    }
-                }
-                if (ok) ok = produce_piece(ring, cur, issued, codes, scales, k, kb);
-            }
-            if (*ring.abort_flag) {
-                drain(ring, cur, issued);
-                const uint64_t t0 = global_timer_ns();
-                while (!mbar_try_wait_sleep_at(xfull, 0) && global_timer_ns() - t0 < kWaitLimitNs / 4) {
-                }
-            }
+            bool ok = true;
+            // Two slots at once, the rest behind the requests for the token rows: rows queued behind
+            // a whole ring of weights arrive 3 us later.
+            auto rows_first = [&](uint32_t n) { if (n == 2) wait(ring, requested, 0); };
+            for (int q = q0; q <= q1 && ok; ++q)
+                ok = produce_piece(ring, cur, issued, a.codes + (size_t)q * a.KT * kTileCodeBytes,
+                                   a.scales + (size_t)q * a.KT * kTileScaleBytes, q == q0 ? k0 : 0, q == q1 ? k1 : a.KT, rows_first);
+            if (*ring.abort_flag) drain(ring, cur, issued);
         }
         return;
     }
 
+    if (threadIdx.x < kMaxTokens) emax[threadIdx.x] = 0;
+    if (threadIdx.x < 64) reinterpret_cast<uint32_t *>(smem + lay.zeros)[threadIdx.x] = 0;
     const bool gated = a.ep.act == TFMOE_ACT_SWIGLU;
     const float g0 = __ldg(a.ep.global0), g1 = gated ? __ldg(a.ep.global1) : 0.f;
+    asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
     grid_dep_wait();                                        // before anything another kernel may write
-    wait(ring, xfull, 0);
-    convert_rows(smem + lay.x, a.T, a.K, a.KT, emax,
-                 [&](int kg) { return (kg * 128 >= xa0 && kg * 128 < xb0) || kg * 128 < xb1; });
+    {
+        const bool all = q1 > q0 + 1;
+        convert_rows<8 * NT>(a.x, a.ldx, smem + lay.x, a.T, a.K, a.KT, emax, [&](int kg) {
+            const bool from = kg >= k0 / 2, to = kg <= (k1 - 1) / 2;
+            return all || (q1 == q0 ? from && to : from || to);
+        }, requested);
+    }
 
     const Lane ln;
     uint32_t xa[NT];
@@ -180,32 +158,38 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
             is_last = atomicAdd(a.tickets + q, 1) == (int)(cb - ca);
             if (is_last) a.tickets[q] = 0;                  // for the next call
             __threadfence();
+            join[threadIdx.x][1] = (int)(2 * ca + (first_unit(ca, U, G) / a.KT != q));
+            join[threadIdx.x][2] = (int)(2 * cb);
         }
-        last[threadIdx.x] = is_last;
+        join[threadIdx.x][0] = is_last;
     }
     consumer_sync();
     for (int p = 0; p < 2; ++p) {
-        if (!last[p]) continue;
-        const uint32_t q = p ? q1 : q0;
-        const uint32_t ca = owner(q * a.KT, U, G), cb = owner((q + 1) * a.KT - 1, U, G);
-        const size_t stride = (size_t)2 * a.T * 32;         // in float4
+        if (!join[p][0]) continue;
+        // the pieces of the tile: only its first CTA can have started before it, so the others' are their first
+        const int pa = join[p][1], pb = join[p][2], stride = a.T * 32;   // in float4
         for (int i = threadIdx.x; i < a.T * 32; i += kConsumerThreads) {
-            // only the first of the tile's CTAs can have started before the tile
-            const float4 *src = reinterpret_cast<const float4 *>(a.partial) + ca * stride + i;
-            float4 v = __ldcg(src + (first_unit(ca, U, G) / a.KT != q) * (stride / 2));
-            for (uint32_t cc = ca + 1; cc <= cb; cc += 4) {
-                float4 p4[4];
+            const float4 *src = reinterpret_cast<const float4 *>(a.partial) + i;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            int s0 = pa;
+            do {
+                float4 p4[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (cc + j <= cb) p4[j] = __ldcg(src + (cc + j - ca) * stride);
+                for (int j = 0; j < 8; ++j) {
+                    const int s1 = j == 0 ? s0 : (s0 & ~1) + 2 * j;
+                    if (s1 <= pb) p4[j] = __ldcg(src + (size_t)s1 * stride);
+                }
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (cc + j <= cb) { v.x += p4[j].x; v.y += p4[j].y; v.z += p4[j].z; v.w += p4[j].w; }
-            }
+                for (int j = 0; j < 8; ++j) {
+                    if ((j == 0 ? s0 : (s0 & ~1) + 2 * j) > pb) continue;
+                    v.x += p4[j].x; v.y += p4[j].y; v.z += p4[j].z; v.w += p4[j].w;
+                }
+                s0 = (s0 & ~1) + 16;
+            } while (s0 <= pb);
             *reinterpret_cast<float4 *>(sums + (i >> 5) * kSumStride + (i & 31) * 4) = v;
         }
         consumer_sync();
-        finish_tile(a, q, sums, nullptr, g0, g1);
+        finish_tile(a, p ? q1 : q0, sums, nullptr, g0, g1);
         consumer_sync();
     }
 }

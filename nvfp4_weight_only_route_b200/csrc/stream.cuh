@@ -50,13 +50,10 @@ __host__ __device__ constexpr uint32_t chunk_offset(int k) {
     return (uint32_t)(k >> 7) * 256u + (uint32_t)(((k >> 3) - (k >> 5)) & 3) * 64u + (uint32_t)((k >> 5) & 3) * 16u;
 }
 
-// First unit of CTA c, and the CTA that owns unit u, when U units are cut into G runs.
-__host__ __device__ __forceinline__ uint32_t first_unit(uint32_t c, uint32_t U, uint32_t G) {
-    return (uint32_t)((uint64_t)c * U / G);
-}
-__host__ __device__ __forceinline__ uint32_t owner(uint32_t u, uint32_t U, uint32_t G) {
-    return (uint32_t)((((uint64_t)u + 1) * G - 1) / U);
-}
+// First unit of CTA c, and the CTA that owns unit u, when U units are cut into G runs. The
+// handles keep U below 2^24 and G is the SM count, so the products fit 32 bits.
+__host__ __device__ __forceinline__ uint32_t first_unit(uint32_t c, uint32_t U, uint32_t G) { return c * U / G; }
+__host__ __device__ __forceinline__ uint32_t owner(uint32_t u, uint32_t U, uint32_t G) { return ((u + 1) * G - 1) / U; }
 
 struct Ring {
     uint32_t slots, full, empty;          // shared addresses
@@ -98,10 +95,13 @@ __device__ __forceinline__ void bulk_at(uint32_t dst, const void *src, uint32_t 
 }
 
 // The producer's side: put the column tiles [ka, kb) of one row tile into the ring, whose codes
-// and scales start at `codes` and `scales` (those of column tile 0). Returns false after an abort.
+// and scales start at `codes` and `scales` (those of column tile 0); before(n) runs ahead of the n-th
+// slot. Returns false after an abort.
+template <class Before>
 __device__ __forceinline__ bool produce_piece(const Ring &r, Cursor &c, uint32_t &issued, const uint8_t *codes,
-                                              const uint8_t *scales, int ka, int kb) {
+                                              const uint8_t *scales, int ka, int kb, Before before) {
     for (int k = ka; k < kb;) {
+        before(issued);
         const int at = k % kWindow, n = min(kWindow - at, kb - k);
         const uint32_t full = r.full + 8u * c.slot, slot = r.slots + (uint32_t)c.slot * kSlotBytes;
         if (issued >= (uint32_t)r.n && !wait(r, r.empty + 8u * c.slot, c.phase ^ 1u)) return false;
@@ -353,47 +353,55 @@ __device__ __forceinline__ float inverse_up(uint32_t emax) {
     return __uint_as_float((uint32_t)(254 - up_field(emax)) << 23);
 }
 
-// Turn T bf16 rows of K values that lie in shared memory (row_bytes(KT) apart) into operand rows in
-// place, by all consumers: the 128-column groups for which used(group) holds become f16 times a power
-// of two per row (exact for every element within 2^28 of the row's largest used one; smaller ones
-// are rounded to 2^-39 of it), with columns from K on zero. emax[t] (zero before) receives the
-// rows' largest exponent fields. Ends with a consumer barrier.
-template <class Used>
-__device__ __forceinline__ void convert_rows(uint8_t *rows, int T, int K, int KT, uint32_t *emax, Used used) {
+// T bf16 rows of K values in global memory (ld apart, 16-byte aligned) become operand rows in shared
+// memory (row_bytes(KT) apart), by all consumers: f16 times a power of two per row (exact for every
+// element within 2^28 of the row's largest; smaller ones are rounded to 2^-39 of it), columns from K
+// on zero. Only the 128-column groups for which used(group) holds are read and written. emax[t] (zero
+// before) receives the rows' largest exponent fields. Ends with a consumer barrier. A thread
+// keeps up to kHeld chunks in registers between finding the maximum and converting; what lies beyond
+// is read again. requested: an
+// mbarrier that every consumer warp arrives at once its first loads are on the way.
+template <int kHeld, class Used>
+__device__ __forceinline__ void convert_rows(const uint16_t *x, int64_t ld, uint8_t *rows, int T, int K, int KT,
+                                             uint32_t *emax, Used used, uint32_t requested = 0) {
     const int chunks = ((KT + 1) / 2) * 16;
     int tpr = kConsumerThreads;                              // threads per row, at least a warp
     while (tpr * T > kConsumerThreads) tpr >>= 1;
     const int t = threadIdx.x / tpr, i0 = threadIdx.x % tpr;
-    uint8_t *row = rows + t * row_bytes(KT);
+    const uint4 *row = reinterpret_cast<const uint4 *>(x + (int64_t)t * ld);
+    uint4 v[kHeld];
+    if (t < T) {
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) {
+            const int i = i0 + j * tpr;
+            v[j] = i * 8 < K && used(i >> 4) ? row[i] : make_uint4(0, 0, 0, 0);
+        }
+    }
+    if (requested && (threadIdx.x & 31) == 0) mbar_arrive_at(requested);
     if (t < T) {
         uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) m = max_bits(v[j], m);
 #pragma unroll 4
-        for (int i = i0; i < chunks; i += tpr)
-            if (i * 8 < K && used(i >> 4)) m = max_bits(*reinterpret_cast<const uint4 *>(row + 16 * i), m);
+        for (int i = i0 + kHeld * tpr; i * 8 < K; i += tpr)
+            if (used(i >> 4)) m = max_bits(row[i], m);
         const uint32_t e = __reduce_max_sync(0xffffffffu, max(m >> 23, (m >> 7) & 0xFFu));
         if ((threadIdx.x & 31) == 0) atomicMax(&emax[t], e);
     }
     consumer_sync();
     if (t < T) {
-        // a half warp turns groups of 16 chunks, each read by its lanes before any writes it
         const float up = up_of(emax[t]);
-        const uint32_t half = 0xFFFFu << (threadIdx.x & 16);
-        for (int i = i0; i < chunks; i += 4 * tpr) {         // chunks and tpr are multiples of 16
-            uint4 v[4];
+        uint8_t *dst = rows + t * row_bytes(KT);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int ij = i + j * tpr;
-                v[j] = make_uint4(0, 0, 0, 0);
-                if (ij * 8 < K && used(ij >> 4)) v[j] = *reinterpret_cast<const uint4 *>(row + 16 * ij);
-            }
-            __syncwarp(half);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int ij = i + j * tpr;
-                if (ij < chunks && used(ij >> 4))
-                    *reinterpret_cast<uint4 *>(row + chunk_offset(ij * 8)) = bf16x8_to_f16(v[j], up);
-            }
+        for (int j = 0; j < kHeld; ++j) {
+            const int i = i0 + j * tpr;
+            if (i < chunks && used(i >> 4)) *reinterpret_cast<uint4 *>(dst + chunk_offset(i * 8)) = bf16x8_to_f16(v[j], up);
         }
+#pragma unroll 4
+        for (int i = i0 + kHeld * tpr; i < chunks; i += tpr)
+            if (used(i >> 4))
+                *reinterpret_cast<uint4 *>(dst + chunk_offset(i * 8)) =
+                    i * 8 < K ? bf16x8_to_f16(row[i], up) : make_uint4(0, 0, 0, 0);
     }
     consumer_sync();
 }
