@@ -187,6 +187,35 @@ TFMOE_API tfmoe_status tfmoe_forward_add_norm(tfmoe_layer *layer, const uint16_t
                                               uint16_t *out, uint16_t *out_norm, void *cuda_stream);
 
 /*
+ * The same layer, residual add and RMS norm for the few tokens of a decode step, in one
+ * kernel: 0 <= T <= TFMOE_DECODE_MAX_TOKENS (and <= max_tokens). Arguments, formats,
+ * alignment, overlap rules and stream behaviour are those of tfmoe_forward_add_norm, and
+ * with residual and norm_w NULL the call computes what tfmoe_forward does. Routing is the
+ * same, bit for bit. What differs:
+ *  - The whole grid works on one call and its CTAs wait for one another (a cooperative
+ *    launch of one CTA per SM): the kernel does not share the GPU with another kernel.
+ *    It may be captured in a CUDA graph.
+ *  - The SwiGLU output a is rounded to 11 significant bits (an f16 times a power of two per
+ *    token and expert) where tfmoe_forward rounds it to bf16, so outputs are closer to the
+ *    unrounded layer, and not bit-equal to tfmoe_forward's. Equal calls give equal bits.
+ *  - The regime flags and gemv_max_tokens do not apply. Of the buffers of tfmoe_get_buffer
+ *    the call writes LOGITS (every entry exact), TOPK_IDS and TOPK_WEIGHTS; the others hold
+ *    what an earlier forward left, and tfmoe_forward_stage has nothing to replay after it.
+ * TFMOE_ERR_UNSUPPORTED when T is above tfmoe_decode_max_tokens(layer): the token operands
+ * have to fit in shared memory, which takes rows of hidden or intermediate above about 4800
+ * elements down from 16 tokens.
+ * The device-side waits are bounded; when one gives up, the output is undefined and
+ * tfmoe_sync_status reports TFMOE_ERR_TIMEOUT.
+ */
+#define TFMOE_DECODE_MAX_TOKENS 16
+TFMOE_API tfmoe_status tfmoe_forward_decode(tfmoe_layer *layer, const uint16_t *x, int32_t T,
+                                            const uint16_t *residual, const uint16_t *norm_w,
+                                            uint16_t *out, uint16_t *out_norm, void *cuda_stream);
+
+/* The largest T tfmoe_forward_decode accepts on this handle (0 for NULL). */
+TFMOE_API int32_t tfmoe_decode_max_tokens(tfmoe_layer *layer);
+
+/*
  * Same computation with HOST buffers: x_host[T][H] is copied to the
  * device, the layer runs, and the result is copied into out_host[T][H];
  * all on `cuda_stream`, and the call returns after the result has arrived

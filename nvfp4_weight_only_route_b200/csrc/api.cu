@@ -95,6 +95,9 @@ void carve_workspace(Layer &L, uint8_t *base, size_t *total) {
     c.take(&w.y, P * H, base);
     c.take(&w.x_stage, T * H, base);
     c.take(&w.out_stage, T * H, base);
+    c.take(&w.dec_gu, decode_gu_floats(L), base);
+    c.take(&w.dec_d, decode_d_floats(L), base);
+    c.take(&w.dec_arrivals, decode_arrival_words(), base);
     *total = align_up(c.off, 256);
 }
 
@@ -209,6 +212,8 @@ tfmoe_status tfmoe_create(const tfmoe_layer_desc *desc, tfmoe_layer **out)
     e = cudaMemset(L.ws.err_word, 0, sizeof(int32_t));
     if (e == cudaSuccess) e = cudaMemset(L.ws.route_counter, 0, sizeof(int32_t));
     if (e == cudaSuccess) e = cudaMemset(L.ws.plan_counter, 0, sizeof(int32_t));
+    if (e == cudaSuccess) e = cudaMemset(L.ws.dec_arrivals, 0, decode_arrival_words() * sizeof(uint32_t));
+    if (e == cudaSuccess) e = decode_setup(L);
     if (e == cudaSuccess) e = gemv_setup(L);
     if (e == cudaSuccess) e = mma_setup(L);
     if (e == cudaSuccess) e = router_setup(L);
@@ -300,11 +305,10 @@ bool overlap(const void *a, const void *b, size_t bytes) {
     return x < y + bytes && y < x + bytes;
 }
 
-// The forward chain; residual, norm_w and out_norm are the optional epilogue (see
-// tfmoe_forward_add_norm), all NULL for tfmoe_forward.
-tfmoe_status forward_impl(tfmoe_layer *layer, const char *who, const uint16_t *x, int32_t T,
-                          const uint16_t *residual, const uint16_t *norm_w, uint16_t *out, uint16_t *out_norm,
-                          void *cuda_stream)
+// The checks of a forward's arguments; residual, norm_w and out_norm are the optional epilogue
+// (see tfmoe_forward_add_norm). Resets out_norm when there are no norm weights.
+tfmoe_status check_forward(tfmoe_layer *layer, const char *who, const uint16_t *x, int32_t T, const uint16_t *residual,
+                           const uint16_t *norm_w, const uint16_t *out, uint16_t **out_norm)
 {
     if (!layer) return fail(TFMOE_ERR_INVALID_ARG, "%s: layer is NULL", who);
     Layer &L = layer->impl;
@@ -314,17 +318,27 @@ tfmoe_status forward_impl(tfmoe_layer *layer, const char *who, const uint16_t *x
         return fail(TFMOE_ERR_INVALID_ARG, "%s: T=%d outside [0, max_tokens=%d]", who, T, L.desc.max_tokens);
     if (T == 0) return ok();
     if (!x || !out) return fail(TFMOE_ERR_INVALID_ARG, "%s: x or out is NULL", who);
-    if (norm_w && !out_norm) return fail(TFMOE_ERR_INVALID_ARG, "%s: norm_w given but out_norm is NULL", who);
-    if (!norm_w) out_norm = nullptr;
-    if (!aligned16(x) || !aligned16(out) || !aligned16(residual) || !aligned16(norm_w) || !aligned16(out_norm))
+    if (norm_w && !*out_norm) return fail(TFMOE_ERR_INVALID_ARG, "%s: norm_w given but out_norm is NULL", who);
+    if (!norm_w) *out_norm = nullptr;
+    if (!aligned16(x) || !aligned16(out) || !aligned16(residual) || !aligned16(norm_w) || !aligned16(*out_norm))
         return fail(TFMOE_ERR_INVALID_ARG, "%s: x, out, residual, norm_w and out_norm must be 16-byte aligned", who);
     const size_t bytes = (size_t)T * L.desc.hidden * 2;
-    if (overlap(x, out, bytes) || overlap(x, out_norm, bytes) || overlap(out, out_norm, bytes) ||
-        overlap(residual, out_norm, bytes) || overlap(residual, x, bytes) ||
+    if (overlap(x, out, bytes) || overlap(x, *out_norm, bytes) || overlap(out, *out_norm, bytes) ||
+        overlap(residual, *out_norm, bytes) || overlap(residual, x, bytes) ||
         (residual != out && overlap(residual, out, bytes)))
         return fail(TFMOE_ERR_INVALID_ARG, "%s: overlapping x / residual / out / out_norm (only residual == out "
                     "is allowed)", who);
+    return ok();
+}
 
+// The forward chain (arguments NULL where there is no epilogue).
+tfmoe_status forward_impl(tfmoe_layer *layer, const char *who, const uint16_t *x, int32_t T,
+                          const uint16_t *residual, const uint16_t *norm_w, uint16_t *out, uint16_t *out_norm,
+                          void *cuda_stream)
+{
+    const tfmoe_status st = check_forward(layer, who, x, T, residual, norm_w, out, &out_norm);
+    if (st != TFMOE_OK || T == 0) return st;
+    Layer &L = layer->impl;
     DeviceGuard dg(L.device);
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
     int n = 0;
@@ -377,6 +391,27 @@ tfmoe_status tfmoe_forward_add_norm(tfmoe_layer *layer, const uint16_t *x, int32
     return forward_impl(layer, "tfmoe_forward_add_norm", x, T, residual, norm_w, out, out_norm, cuda_stream);
 }
 
+tfmoe_status tfmoe_forward_decode(tfmoe_layer *layer, const uint16_t *x, int32_t T, const uint16_t *residual,
+                                  const uint16_t *norm_w, uint16_t *out, uint16_t *out_norm, void *cuda_stream)
+{
+    const char *who = "tfmoe_forward_decode";
+    const tfmoe_status st = check_forward(layer, who, x, T, residual, norm_w, out, &out_norm);
+    if (st != TFMOE_OK || T == 0) return st;
+    Layer &L = layer->impl;
+    if (T > decode_max_tokens(L))
+        return fail(TFMOE_ERR_UNSUPPORTED, "%s: T=%d above this handle's limit of %d tokens (tfmoe_decode_max_tokens)",
+                    who, T, decode_max_tokens(L));
+    DeviceGuard dg(L.device);
+    int n = 0;
+    const cudaError_t e = launch_decode(L, x, T, residual, norm_w, out, out_norm, static_cast<cudaStream_t>(cuda_stream), &n);
+    L.last_launches = n;
+    L.last_T = -1;                       // no stages to replay: the chain's intermediates are not this call's
+    if (e != cudaSuccess) return cuda_fail(e, who);
+    return ok();
+}
+
+int32_t tfmoe_decode_max_tokens(tfmoe_layer *layer) { return layer ? decode_max_tokens(layer->impl) : 0; }
+
 tfmoe_status tfmoe_forward_host(tfmoe_layer *layer, const uint16_t *x_host, int32_t T, uint16_t *out_host,
                                 void *cuda_stream)
 {
@@ -411,6 +446,8 @@ tfmoe_status tfmoe_sync_status(tfmoe_layer *layer, void *cuda_stream)
     int32_t word = 0;
     e = cudaMemcpy(&word, L.ws.err_word, sizeof word, cudaMemcpyDeviceToHost);
     if (e == cudaSuccess && word != 0) e = cudaMemset(L.ws.err_word, 0, sizeof(int32_t));
+    if (e == cudaSuccess && (word & DEV_ERR_WAIT_TIMEOUT))
+        e = cudaMemset(L.ws.dec_arrivals, 0, decode_arrival_words() * sizeof(uint32_t));
     if (e != cudaSuccess) return cuda_fail(e, "tfmoe_sync_status: error word");
     if (word & DEV_ERR_WAIT_TIMEOUT) return fail(TFMOE_ERR_TIMEOUT, "a device-side wait timed out (word 0x%x)", word);
     if (word) return fail(TFMOE_ERR_DEVICE, "device error word 0x%x (1 bad expert id, 2 bad row, 8 non-finite logit)", word);

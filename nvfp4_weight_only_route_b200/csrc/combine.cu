@@ -67,17 +67,6 @@ __global__ void __launch_bounds__(256) combine_kernel(
     *reinterpret_cast<uint4 *>(out + (size_t)t * H + h) = pack_bf16x8(acc);
 }
 
-// Correctly rounded fp64 -> bf16 (nearest, ties to even): round to fp32 toward zero and
-// make the result odd when that step was inexact ("round to odd"), then round that fp32
-// to bf16. fp32 keeps 16 more significand bits than bf16, so the second rounding sees the
-// true position of the value between its two bf16 neighbours (Boldo and Melquiond's
-// round-to-odd method).
-__device__ __forceinline__ uint16_t double_to_bf16_bits_rn(double d) {
-    float f = __double2float_rz(d);
-    if ((double)f != d && f == f) f = __uint_as_float(__float_as_uint(f) | 1u);
-    return float_to_bf16_bits_rn(f);
-}
-
 // One CTA per token: the combine (as combine_kernel) into out, kept in shared memory; the
 // fp64 sum of squares of the rounded row; then out_norm = bf16(out * gamma * r) with
 // r = 1 / sqrt(sum / H + eps), the products in fp64.

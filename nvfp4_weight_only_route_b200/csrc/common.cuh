@@ -154,6 +154,17 @@ __device__ __forceinline__ uint16_t float_to_bf16_bits_rn(float f) {
     return *reinterpret_cast<uint16_t *>(&b);
 }
 
+// Correctly rounded fp64 -> bf16 (nearest, ties to even): round to fp32 toward zero and
+// make the result odd when that step was inexact ("round to odd"), then round that fp32
+// to bf16. fp32 keeps 16 more significand bits than bf16, so the second rounding sees the
+// true position of the value between its two bf16 neighbours (Boldo and Melquiond's
+// round-to-odd method).
+__device__ __forceinline__ uint16_t double_to_bf16_bits_rn(double d) {
+    float f = __double2float_rz(d);
+    if ((double)f != d && f == f) f = __uint_as_float(__float_as_uint(f) | 1u);
+    return float_to_bf16_bits_rn(f);
+}
+
 // Sixteen bf16 values -> f16 values times 2^sh, sh chosen from the block's largest
 // exponent so that the largest magnitude lands in [2^14, 2^15). Every bf16 element
 // within 2^28 of the block's largest is then an exact f16 (its 8-bit significand stays

@@ -92,6 +92,9 @@ struct Workspace {
     float *y = nullptr;             // [maxP][H]
     uint16_t *x_stage = nullptr;    // [maxT][H] bf16, for forward_host
     uint16_t *out_stage = nullptr;  // [maxT][H] bf16, for forward_host
+    float *dec_gu = nullptr;        // one-kernel decode: sums of the gate/up pieces
+    float *dec_d = nullptr;         // one-kernel decode: sums of the down pieces
+    uint32_t *dec_arrivals = nullptr; // one-kernel decode: grid barrier counters
 };
 
 struct Weights {
@@ -191,6 +194,16 @@ void mma_teardown(Layer &L);
 cudaError_t launch_gather(Layer &L, const uint16_t *x, int T, cudaStream_t s, int *launches);
 cudaError_t launch_mma_gate_up(Layer &L, cudaStream_t s, int *launches);
 cudaError_t launch_mma_down(Layer &L, cudaStream_t s, int *launches);
+
+// The whole layer for a few tokens in one kernel (decode.cu): the largest T, the workspace's
+// sizes, and the launch (arguments as tfmoe_forward_decode).
+int decode_max_tokens(const Layer &L);
+size_t decode_gu_floats(const Layer &L);
+size_t decode_d_floats(const Layer &L);
+size_t decode_arrival_words();
+cudaError_t decode_setup(const Layer &L);
+cudaError_t launch_decode(Layer &L, const uint16_t *x, int T, const uint16_t *residual, const uint16_t *norm_w,
+                          uint16_t *out, uint16_t *out_norm, cudaStream_t s, int *launches);
 
 // cuTensorMapEncodeTiled for a 2-D tensor (dim0 contiguous), resolved through the
 // runtime's driver entry point so the library does not link the driver library.

@@ -32,7 +32,7 @@ BUF_LOGITS, BUF_TOPK_IDS, BUF_TOPK_WEIGHTS, BUF_EXPERT_COUNTS, BUF_EXPERT_OFFSET
 EXPORTED = ["tfmoe_create", "tfmoe_load_weights", "tfmoe_forward", "tfmoe_forward_host", "tfmoe_sync_status",
             "tfmoe_destroy", "tfmoe_last_error", "tfmoe_get_buffer", "tfmoe_last_launch_count",
             "tfmoe_profile_enable", "tfmoe_profile_read", "tfmoe_route_noalloc", "tfmoe_forward_stage",
-            "tfmoe_forward_add_norm", "tfmoe_linear_create", "tfmoe_linear_load_weights", "tfmoe_linear_forward",
+            "tfmoe_forward_add_norm", "tfmoe_forward_decode", "tfmoe_decode_max_tokens", "tfmoe_linear_create", "tfmoe_linear_load_weights", "tfmoe_linear_forward",
             "tfmoe_linear_sync_status", "tfmoe_linear_last_launch_count", "tfmoe_linear_destroy"]
 
 ROUTE_NOALLOC_MAX_LOGITS = 1 << 20
@@ -94,6 +94,10 @@ def load_library(path: str = LIB_PATH):
     lib.tfmoe_forward.restype = ctypes.c_int
     lib.tfmoe_forward_add_norm.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp]
     lib.tfmoe_forward_add_norm.restype = ctypes.c_int
+    lib.tfmoe_forward_decode.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp]
+    lib.tfmoe_forward_decode.restype = ctypes.c_int
+    lib.tfmoe_decode_max_tokens.argtypes = [vp]
+    lib.tfmoe_decode_max_tokens.restype = i32
     lib.tfmoe_forward_host.argtypes = [vp, vp, i32, vp, vp]
     lib.tfmoe_forward_host.restype = ctypes.c_int
     lib.tfmoe_sync_status.argtypes = [vp, vp]
@@ -195,6 +199,29 @@ class MoELayer:
                                               _ptr(out_norm) if norm_w is not None else None,
                                               _stream_handle(stream)))
         return out, (out_norm if norm_w is not None else None)
+
+    def decode_max_tokens(self) -> int:
+        """The largest T forward_decode accepts."""
+        return int(self.lib.tfmoe_decode_max_tokens(self.handle))
+
+    def forward_decode(self, x, residual=None, norm_w=None, out=None, out_norm=None, T: Optional[int] = None,
+                       stream=None):
+        """The layer, + residual (may be out itself), and with norm_w the RMS norm of the result, for a
+        decode step's few tokens in one kernel (tfmoe_forward_decode). Returns (out, out_norm or None)."""
+        import torch
+        if T is None:
+            T = x.shape[0]
+        if out is None:
+            out = torch.empty((T, self.desc.hidden), dtype=torch.bfloat16, device=x.device)
+        if norm_w is None:
+            out_norm = None
+        elif out_norm is None:
+            out_norm = torch.empty((T, self.desc.hidden), dtype=torch.bfloat16, device=x.device)
+        if stream is None:
+            stream = torch.cuda.current_stream(x.device)
+        check(self.lib.tfmoe_forward_decode(self.handle, x.data_ptr(), T, _ptr(residual), _ptr(norm_w),
+                                            out.data_ptr(), _ptr(out_norm), stream.cuda_stream))
+        return out, out_norm
 
     def forward_raw(self, x_ptr: int, T: int, out_ptr: int, stream_handle: int) -> int:
         return self.lib.tfmoe_forward(self.handle, x_ptr, T, out_ptr, stream_handle)
