@@ -72,9 +72,11 @@ struct Plan {
     int32_t ids[kMaxPairs];
     float w[kMaxPairs];
     uint32_t sel[kMaxTokens][8];                         // experts of a token, one bit each
+    uint8_t slot[kMaxTokens][256];                       // a token's slot for each of its experts
     int16_t list[256], poff[256], eidx[256];             // active experts; their first row; place in the list
     uint8_t cnt[256];                                    // their tokens
     uint8_t tok[kMaxPairs];                              // token of a row
+    uint8_t ei[kMaxPairs];                               // place in the list of a row's expert
     int16_t row[kMaxPairs];                              // row of a pair
     int n_act;
 };
@@ -84,6 +86,12 @@ struct Plan {
 // by T >= m, so the pieces, at most RT * pairs + G * T columns in all, do not overlap.
 __device__ __forceinline__ size_t piece_at(int poff, int RT, int rt, int m, uint32_t c, int T) {
     return (size_t)(uint32_t)(poff * RT + rt * m + (int)c * T) * 128u;
+}
+
+// The runs of a phase: no more of them than windows, so that a small layer is not cut into pieces whose
+// joining costs more than their reading.
+__device__ __forceinline__ Runs runs_of(int units, uint32_t G) {
+    return Runs((uint32_t)units, min(G, (uint32_t)(units + kWindow - 1) / kWindow));
 }
 
 __device__ __forceinline__ void grid_arrive(uint32_t *counter) {
@@ -168,118 +176,122 @@ __device__ void router_logits(const DecodeArgs &a, double *part) {
     }
 }
 
-// Top k of every token and the plan of the call.
+// Top k of every token (a warp each) and the plan of the call (a thread per expert).
 __device__ void make_plan(const DecodeArgs &a, Plan &pl) {
-    const int warp = threadIdx.x >> 5, tid = threadIdx.x, kx = a.k + a.m;
-    if (warp < a.T) topk_warp(a.logits + (size_t)warp * a.E, a.E, a.k, pl.ids + warp * kx, pl.w + warp * kx, nullptr, a.m);
-    consumer_sync();
-    const bool pair = tid < a.T * kx;
-    const int t = tid / kx, e = pair ? pl.ids[tid] : 0;
-    if (pair) {
-        atomicOr(&pl.sel[t][e >> 5], 1u << (e & 31));
-        if (blockIdx.x == 0) {
-            a.ids[tid] = e;
-            a.topk_w[tid] = pl.w[tid];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x, kx = a.k + a.m;
+    if (warp < a.T) {
+        int id;
+        float w;
+        topk_select(a.logits + (size_t)warp * a.E, a.E, a.k, id, w);
+        if (lane >= a.k) { id = a.E + lane - a.k; w = 1.f; }
+        if (lane < kx) {
+            const int p = warp * kx + lane;
+            pl.ids[p] = id;
+            pl.w[p] = w;
+            pl.slot[warp][id] = (uint8_t)lane;
+            atomicOr(&pl.sel[warp][id >> 5], 1u << (id & 31));
+            if (blockIdx.x == 0) {
+                a.ids[p] = id;
+                a.topk_w[p] = w;
+            }
         }
     }
     consumer_sync();
     if (tid < 256) {                                     // expert tid: its place, first row and tokens
         const int word = tid >> 5;
-        const uint32_t below = (1u << (tid & 31)) - 1u;
-        int idx = 0, rows = 0, n = 0;
-        for (int w = 0; w <= word; ++w) {
-            uint32_t any = 0;
+        const uint32_t below = (1u << lane) - 1u;
+        // lane l < 8: the active experts of word l and their rows; a scan gives those before each word
+        uint32_t any = 0, mine = 0, n = 0;
+        int rows = 0;
+        if (lane < 8)
+#pragma unroll 4
             for (int i = 0; i < a.T; ++i) {
-                const uint32_t s = pl.sel[i][w];
+                const uint32_t s = pl.sel[i][lane];
                 any |= s;
-                rows += __popc(w < word ? s : s & below);
-                if (w == word) n += (s >> (tid & 31)) & 1u;
+                n += (uint32_t)__popc(s) << 16;
             }
-            idx += __popc(w < word ? any : any & below);
+        n += __popc(any);
+        uint32_t incl = n;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
         }
-        if (n) {
+        const uint32_t before = __shfl_sync(0xffffffffu, incl - n, word), own = __shfl_sync(0xffffffffu, any, word);
+        if (tid == 7) pl.n_act = (int)(incl & 0xffffu);
+        rows = (int)(before >> 16);
+        const int idx = (int)(before & 0xffffu) + __popc(own & below);
+#pragma unroll 4
+        for (int i = 0; i < a.T; ++i) {
+            const uint32_t s = pl.sel[i][word];
+            rows += __popc(s & below);
+            mine |= ((s >> lane) & 1u) << i;
+        }
+        if (mine) {
             pl.list[idx] = (int16_t)tid;
-            pl.cnt[idx] = (uint8_t)n;
+            pl.cnt[idx] = (uint8_t)__popc(mine);
             pl.poff[idx] = (int16_t)rows;
             pl.eidx[tid] = (int16_t)idx;
+            for (int r = rows; mine; mine &= mine - 1, ++r) {
+                const int t = __ffs(mine) - 1;
+                pl.tok[r] = (uint8_t)t;
+                pl.ei[r] = (uint8_t)idx;
+                pl.row[t * kx + pl.slot[t][tid]] = (int16_t)r;
+            }
         }
-        if (tid == 255) pl.n_act = idx + (n ? 1 : 0);
-    }
-    consumer_sync();
-    if (pair) {
-        int col = 0;
-        for (int i = 0; i < t; ++i) col += (pl.sel[i][e >> 5] >> (e & 31)) & 1u;
-        const int r = pl.poff[pl.eidx[e]] + col;
-        pl.tok[r] = (uint8_t)t;
-        pl.row[tid] = (int16_t)r;
     }
     consumer_sync();
 }
 
 // One piece through the consumers: the sums of m columns, times factor(column), to dst [m][128].
 template <int NT, class RowOf, class Factor>
-__device__ __forceinline__ void run_piece(const Ring &r, Cursor &c, const Lane &ln, int ka, int kb, int m, RowOf row_of,
-                                          Factor factor, float *buf, float *dst) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+__device__ __forceinline__ void run_piece(Consumer<NT> &in, const Pieces &p, int m, RowOf row_of, Factor factor, float *buf,
+                                          float *dst) {
+    const int g = (threadIdx.x & 31) >> 2;
     uint32_t xa[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) xa[n] = row_of(8 * n + g < m ? 8 * n + g : 0);
     Acc<NT> acc;
     acc.clear();
-    consume_piece<NT>(r, c, ln, ka, kb, xa, acc);
-    // the second half's sums go through shared memory (two buffers in turn, so one barrier per piece)
-    const int row = (warp & 7) * 16 + g;
-    if (warp >= 8) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int col = 8 * n + 2 * t + (j & 1);
-                if (col < m) buf[col * kSumStride + row + 8 * (j >> 1)] = acc.sum(n, j);
-            }
-    }
-    consumer_sync();
-    if (warp < 8) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int col = 8 * n + 2 * t + (j & 1), rr = row + 8 * (j >> 1);
-                if (col < m) dst[col * 128 + rr] = (acc.sum(n, j) + buf[col * kSumStride + rr]) * factor(col);
-            }
-    }
+    in.piece(p.ka, p.kb, p.more(), xa, m > 8, acc);
+    join_pairs<NT>(acc, buf, m, [&](int col, int row, float v) {
+        if (col < m) dst[col * 128 + row] = v * factor(col);
+    });
 }
 
-// a = silu(G) U of the m tokens of list entry ei as operand rows, from the gate/up pieces.
-__device__ void prepare_a(const DecodeArgs &a, const Plan &pl, int ei, uint32_t U1, uint32_t G, uint8_t *rows,
-                          uint32_t *emax, uint32_t *emax_next) {
+// a = silu(G) U of the plan's rows [ra, rb) as operand rows 0, 1, ..., from the gate/up pieces.
+__device__ void prepare_a(const DecodeArgs &a, const Plan &pl, int ra, int rb, const Runs &r1, uint8_t *rows, uint32_t *emax) {
     const int RT = a.I / 64, KT = a.H / kTileK, KT2 = a.I / kTileK, half = a.I / 2;
-    const int m = pl.cnt[ei], poff = pl.poff[ei], e = pl.list[ei];
-    const float g0 = __ldg(a.gate_global + e), g1 = __ldg(a.up_global + e);
-    // item: two neighbouring outputs of one column; a warp's 32 items share the column and the row tile
+    const size_t stride = (size_t)a.T * 32;              // from a tile's piece to its next, in float4
+    // an item is two neighbouring outputs of one row; a warp's 32 items share the row and the row tile
     auto value = [&](int item) {
-        const int col = item / half, jp = item - col * half, rt = jp >> 5;
-        const uint32_t q = (uint32_t)(ei * RT + rt) * (uint32_t)KT;
-        const uint32_t ca = owner(q, U1, G), cb = owner(q + KT - 1, U1, G);
-        const float4 *src = reinterpret_cast<const float4 *>(a.gu_part + piece_at(poff, RT, rt, m, ca, a.T) + col * 128) + (jp & 31);
-        float4 s = __ldcg(src);
-#pragma unroll 4
-        for (uint32_t c = ca + 1; c <= cb; ++c) {
-            const float4 v = __ldcg(src + (size_t)(c - ca) * a.T * 32);
-            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-        }
+        const int r = item / half, jp = item - r * half, rt = jp >> 5, ei = pl.ei[ra + r], e = pl.list[ei];
+        const float g0 = __ldg(a.gate_global + e), g1 = __ldg(a.up_global + e);
+        const uint32_t q = (uint32_t)(ei * RT + rt) * (uint32_t)KT, ca = r1.owner(q), n = r1.owner(q + KT - 1) - ca + 1;
+        const float4 *p = reinterpret_cast<const float4 *>(a.gu_part + piece_at(pl.poff[ei], RT, rt, pl.cnt[ei], ca, a.T) +
+                                                           (ra + r - pl.poff[ei]) * 128) + (jp & 31);
+        float4 v[4], s = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](const float4 &u) { s.x += u.x; s.y += u.y; s.z += u.z; s.w += u.w; };
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i == 0 || i < (int)n) v[i] = __ldcg(p + i * stride);
+        s = v[0];
+#pragma unroll
+        for (int i = 1; i < 4; ++i)
+            if (i < (int)n) add(v[i]);
+        for (uint32_t i = 4; i < n; ++i) add(__ldcg(p + i * stride));
         return make_float2(silu_f32(s.x * g0) * (s.y * g1), silu_f32(s.z * g0) * (s.w * g1));
     };
-    constexpr int kHold = 4;
+    constexpr int kHold = 3;
     float2 hold[kHold];
-    const int items = m * half;
+    const int items = (rb - ra) * half;
     auto note = [&](int item, float2 v) {
         const uint32_t bits = max(__float_as_uint(v.x) & 0x7FFFFFFFu, __float_as_uint(v.y) & 0x7FFFFFFFu);
         const uint32_t b = __reduce_max_sync(0xffffffffu, bits >> 23);
         if ((threadIdx.x & 31) == 0) atomicMax(&emax[item / half], b);
     };
-    consumer_sync();                                     // the rows and the other exponents are free
-    if (threadIdx.x < kMaxTokens) emax_next[threadIdx.x] = 0;
+    for (int i = threadIdx.x; i < rb - ra; i += kConsumerThreads) emax[i] = 0;
+    consumer_sync();
 #pragma unroll
     for (int j = 0; j < kHold; ++j) {
         const int item = threadIdx.x + j * kConsumerThreads;
@@ -293,9 +305,9 @@ __device__ void prepare_a(const DecodeArgs &a, const Plan &pl, int ei, uint32_t 
     for (int item = threadIdx.x + kHold * kConsumerThreads; item < items; item += kConsumerThreads) note(item, value(item));
     consumer_sync();
     auto put = [&](int item, float2 v) {
-        const int col = item / half, j = 2 * (item - col * half);
-        const float up = up_of(emax[col]);
-        *reinterpret_cast<__half2 *>(rows + col * row_bytes(KT2) + chunk_offset(j & ~7) + (j & 7) * 2) =
+        const int r = item / half, j = 2 * (item - r * half);
+        const float up = up_of(emax[r]);
+        *reinterpret_cast<__half2 *>(rows + r * row_bytes(KT2) + chunk_offset(j & ~7) + (j & 7) * 2) =
             __floats2half2_rn(v.x * up, v.y * up);
     };
 #pragma unroll
@@ -308,41 +320,49 @@ __device__ void prepare_a(const DecodeArgs &a, const Plan &pl, int ei, uint32_t 
 }
 
 // The weighted sum of token t's slots (plus the residual) at h = 64 hb + 2 lane and h + 1, by one warp.
-__device__ __forceinline__ float2 combine64(const DecodeArgs &a, const Plan &pl, int t, int hb, uint32_t U2, uint32_t G) {
+__device__ __forceinline__ float2 combine64(const DecodeArgs &a, const Plan &pl, int t, int hb, const Runs &r2) {
     const int lane = threadIdx.x & 31, kx = a.k + a.m, RT = a.H / kTileRows, KT = a.I / kTileK, rt = hb >> 1;
     // lane s finds the pieces of slot s
     uint32_t base = 0, n = 0;
     float w = 0.f;
     if (lane < kx) {
         const int p = t * kx + lane, ei = pl.eidx[pl.ids[p]], poff = pl.poff[ei], m = pl.cnt[ei];
-        const uint32_t q = (uint32_t)(ei * RT + rt) * (uint32_t)KT;
-        const uint32_t ca = owner(q, U2, G), cb = owner(q + KT - 1, U2, G);
+        const uint32_t q = (uint32_t)(ei * RT + rt) * (uint32_t)KT, ca = r2.owner(q);
         base = (uint32_t)(piece_at(poff, RT, rt, m, ca, a.T) + (pl.row[p] - poff) * 128);
-        n = cb - ca + 1;
+        n = r2.owner(q + KT - 1) - ca + 1;
         w = pl.w[p];
     }
-    const uint32_t col = (uint32_t)(hb & 1) * 64u + 2u * lane;
+    const uint32_t col = (uint32_t)(hb & 1) * 64u + 2u * lane, most = __reduce_max_sync(0xffffffffu, n);
     float2 acc = make_float2(0.f, 0.f);
     for (int s0 = 0; s0 < kx; s0 += 8) {
-        float2 v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t b = __shfl_sync(0xffffffffu, base, (s0 + j) & 31);
-            if (s0 + j < kx) v[j] = __ldcg(reinterpret_cast<const float2 *>(a.d_part + b + col));
-        }
+        float2 v[8], u[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const uint32_t b = __shfl_sync(0xffffffffu, base, (s0 + j) & 31), c = __shfl_sync(0xffffffffu, n, (s0 + j) & 31);
-            const float g = __shfl_sync(0xffffffffu, w, (s0 + j) & 31);
-            if (s0 + j >= kx) continue;
-#pragma unroll 2
-            for (uint32_t i = 1; i < c; ++i) {
-                const float2 u = __ldcg(reinterpret_cast<const float2 *>(a.d_part + b + i * a.T * 128u + col));
-                v[j].x += u.x;
-                v[j].y += u.y;
+            v[j] = u[j] = make_float2(0.f, 0.f);
+            const float2 *src = reinterpret_cast<const float2 *>(a.d_part + b + col);
+            if (s0 + j < kx && c > 0) v[j] = __ldcg(src);
+            if (s0 + j < kx && c > 1) u[j] = __ldcg(src + a.T * 64);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) { v[j].x += u[j].x; v[j].y += u[j].y; }
+        for (uint32_t i = 2; i < most; ++i) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t b = __shfl_sync(0xffffffffu, base, (s0 + j) & 31), c = __shfl_sync(0xffffffffu, n, (s0 + j) & 31);
+                u[j] = make_float2(0.f, 0.f);
+                if (s0 + j < kx && i < c) u[j] = __ldcg(reinterpret_cast<const float2 *>(a.d_part + b + i * a.T * 128u + col));
             }
-            acc.x = fmaf(g, v[j].x, acc.x);
-            acc.y = fmaf(g, v[j].y, acc.y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) { v[j].x += u[j].x; v[j].y += u[j].y; }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float g = __shfl_sync(0xffffffffu, w, (s0 + j) & 31);
+            if (s0 + j < kx) {
+                acc.x = fmaf(g, v[j].x, acc.x);
+                acc.y = fmaf(g, v[j].y, acc.y);
+            }
         }
     }
     if (a.residual) {
@@ -359,12 +379,13 @@ struct Layout {
         rows = (uint32_t)slots * kSlotBytes;
         sums = rows + (uint32_t)T * row_bytes(KT1 > KT2 ? KT1 : KT2);
         zeros = sums + 2u * T * kSumStride * 4;
-        emax = zeros + 256;                              // x rows, a rows of the experts in turn
-        bars = emax + 3 * kMaxTokens * 4;
+        emax = zeros + 256;                              // of the x rows and the a rows
+        bars = emax + (kMaxTokens + kMaxPairs) * 4;
         total = bars + (2 * kMaxSlots + 3) * 8;          // full, empty, planned, never, abort flag
     }
 };
 
+template <int NT>
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
 {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -397,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
         fence_mbar_init();
     }
     if (threadIdx.x < kMaxTokens * 8) reinterpret_cast<uint32_t *>(pl.sel)[threadIdx.x] = 0;
-    if (threadIdx.x < 3 * kMaxTokens) reinterpret_cast<uint32_t *>(smem + lay.emax)[threadIdx.x] = 0;
+    if (threadIdx.x < kMaxTokens) reinterpret_cast<uint32_t *>(smem + lay.emax)[threadIdx.x] = 0;
     if (threadIdx.x < 64) reinterpret_cast<uint32_t *>(smem + lay.zeros)[threadIdx.x] = 0;
     __syncthreads();
 
@@ -408,15 +429,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
             bool ok = true;
             auto nothing = [](uint32_t) {};
             auto run = [&](const uint8_t *codes, const uint8_t *scales, int RT, int KT) {
-                const uint32_t U = (uint32_t)pl.n_act * RT * KT, Gs = min(G, U);
-                const uint32_t u1 = c < Gs ? first_unit(c + 1, U, Gs) : 0u;
-                for (uint32_t u = first_unit(c, U, Gs); u < u1 && ok;) {
-                    const uint32_t q = u / KT, ei = q / RT;
-                    const int ka = (int)(u - q * KT), kb = (int)min((uint32_t)KT, ka + (u1 - u));
-                    const size_t tile = ((size_t)pl.list[ei] * RT + (q - ei * RT)) * KT;
-                    ok = produce_piece(ring, cur, issued, codes + tile * kTileCodeBytes, scales + tile * kTileScaleBytes, ka,
-                                       kb, nothing);
-                    u += kb - ka;
+                const Runs r = runs_of(pl.n_act * RT * KT, G);
+                for (Pieces p(r.first(c), r.end(c), RT, KT); p.valid() && ok; p.next()) {
+                    const size_t tile = ((size_t)pl.list[p.ei] * RT + p.rt) * KT;
+                    ok = produce_piece(ring, cur, issued, codes + tile * kTileCodeBytes, scales + tile * kTileScaleBytes, p.ka,
+                                       p.kb, nothing);
                 }
             };
             run(a.gu_codes, a.gu_scales, RT1, KT1);
@@ -449,54 +466,49 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
     make_plan(a, pl);
     if (threadIdx.x == 0) mbar_arrive_at(planned);
 
-    const Lane ln;
-    Cursor cur;
-    int buf = 0;
-    const uint32_t U1 = (uint32_t)pl.n_act * RT1 * KT1, U2 = (uint32_t)pl.n_act * RT2 * KT2;
-    // the CTAs that stream: no more than there are units, so that each has some
-    const uint32_t G1 = min(G, U1), G2 = min(G, U2);
+    Consumer<NT> in(ring);
+    int turn = 0;                                        // which buffer of sums
+    const Runs r1 = runs_of(pl.n_act * RT1 * KT1, G), r2 = runs_of(pl.n_act * RT2 * KT2, G);
     const uint32_t rows_at = ring.slots + lay.rows;
     {
-        const uint32_t u1 = c < G1 ? first_unit(c + 1, U1, G1) : 0u, rb = row_bytes(KT1);
-        for (uint32_t u = first_unit(c, U1, G1); u < u1;) {
-            const uint32_t q = u / KT1, ei = q / RT1;
-            const int rt = (int)(q - ei * RT1), ka = (int)(u - q * KT1), kb = (int)min((uint32_t)KT1, ka + (u1 - u));
-            const int m = pl.cnt[ei], poff = pl.poff[ei];
-            auto row_of = [&](int col) { return rows_at + pl.tok[poff + col] * rb; };
-            auto factor = [&](int col) { return inverse_up(emax[pl.tok[poff + col]]); };
-            float *dst = a.gu_part + piece_at(poff, RT1, rt, m, c, a.T), *sb = sums + buf * a.T * kSumStride;
-            if (m <= 8) run_piece<1>(ring, cur, ln, ka, kb, m, row_of, factor, sb, dst);
-            else run_piece<2>(ring, cur, ln, ka, kb, m, row_of, factor, sb, dst);
-            buf ^= 1;
-            u += kb - ka;
+        const uint32_t rb = row_bytes(KT1);
+        Pieces p(r1.first(c), r1.end(c), RT1, KT1);
+        if (p.valid()) in.fetch();
+        for (; p.valid(); p.next()) {
+            const int m = pl.cnt[p.ei], poff = pl.poff[p.ei];
+            run_piece<NT>(in, p, m, [&](int col) { return rows_at + pl.tok[poff + col] * rb; },
+                          [&](int col) { return inverse_up(emax[pl.tok[poff + col]]); }, sums + turn * a.T * kSumStride,
+                          a.gu_part + piece_at(poff, RT1, p.rt, m, c, a.T));
+            turn ^= 1;
         }
     }
     grid_arrive(arrive1);
     grid_wait(ring, arrive1, G);
     if (c == 0 && threadIdx.x == 0) *arrive0 = 0;
     {
-        const uint32_t u1 = c < G2 ? first_unit(c + 1, U2, G2) : 0u, rb = row_bytes(KT2);
-        int have = -1, set = 0;
-        float dg = 0.f;
-        for (uint32_t u = first_unit(c, U2, G2); u < u1;) {
-            const uint32_t q = u / KT2;
-            const int ei = (int)(q / RT2);
-            const int rt = (int)(q - (uint32_t)ei * RT2), ka = (int)(u - q * KT2), kb = (int)min((uint32_t)KT2, ka + (u1 - u));
-            const int m = pl.cnt[ei], poff = pl.poff[ei];
-            if (ei != have) {
-                have = ei;
-                set ^= 1;
-                dg = __ldg(a.down_global + pl.list[ei]);
-                prepare_a(a, pl, ei, U1, G1, rows, emax + (1 + set) * kMaxTokens, emax + (2 - set) * kMaxTokens);
+        const uint32_t rb = row_bytes(KT2);
+        // the rows of as many of the run's experts as fit are prepared together
+        const int fit = (int)((uint32_t)a.T * row_bytes(KT1 > KT2 ? KT1 : KT2) / rb);
+        int r0 = 0, r_end = 0;
+        uint32_t *ea = emax + kMaxTokens;
+        Pieces p(r2.first(c), r2.end(c), RT2, KT2);
+        if (p.valid()) in.fetch();
+        for (; p.valid(); p.next()) {
+            const int m = pl.cnt[p.ei], poff = pl.poff[p.ei];
+            if (poff >= r_end) {
+                const int last = (int)((p.end - 1) / ((uint32_t)RT2 * KT2));
+                int el = p.ei;
+                while (el < last && pl.poff[el + 1] + pl.cnt[el + 1] - poff <= fit) ++el;
+                r0 = poff;
+                r_end = pl.poff[el] + pl.cnt[el];
+                consumer_sync();                         // the rows in use are free
+                prepare_a(a, pl, r0, r_end, r1, rows, ea);
             }
-            const uint32_t *ea = emax + (1 + set) * kMaxTokens;
-            auto row_of = [&](int col) { return rows_at + (uint32_t)col * rb; };
-            auto factor = [&](int col) { return inverse_up(ea[col]) * dg; };
-            float *dst = a.d_part + piece_at(poff, RT2, rt, m, c, a.T), *sb = sums + buf * a.T * kSumStride;
-            if (m <= 8) run_piece<1>(ring, cur, ln, ka, kb, m, row_of, factor, sb, dst);
-            else run_piece<2>(ring, cur, ln, ka, kb, m, row_of, factor, sb, dst);
-            buf ^= 1;
-            u += kb - ka;
+            const float dg = __ldg(a.down_global + pl.list[p.ei]);
+            run_piece<NT>(in, p, m, [&](int col) { return rows_at + (uint32_t)(poff - r0 + col) * rb; },
+                          [&](int col) { return inverse_up(ea[poff - r0 + col]) * dg; }, sums + turn * a.T * kSumStride,
+                          a.d_part + piece_at(poff, RT2, p.rt, m, c, a.T));
+            turn ^= 1;
         }
     }
     grid_arrive(arrive2);
@@ -507,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
     if (!a.norm_w) {
         for (int i = (int)c * kConsumers + warp; i < a.T * blocks; i += (int)G * kConsumers) {
             const int t = i / blocks, hb = i - t * blocks;
-            const float2 v = combine64(a, pl, t, hb, U2, G2);
+            const float2 v = combine64(a, pl, t, hb, r2);
             *reinterpret_cast<uint32_t *>(a.out + (size_t)t * a.H + hb * 64 + 2 * lane) =
                 (uint32_t)float_to_bf16_bits_rn(v.x) | ((uint32_t)float_to_bf16_bits_rn(v.y) << 16);
         }
@@ -518,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
         uint32_t *keep = reinterpret_cast<uint32_t *>(rows);
         double ss = 0.0;
         for (int hb = warp; hb < blocks; hb += kConsumers) {
-            const float2 v = combine64(a, pl, t, hb, U2, G2);
+            const float2 v = combine64(a, pl, t, hb, r2);
             const uint32_t lo = float_to_bf16_bits_rn(v.x), hi = float_to_bf16_bits_rn(v.y);
             *reinterpret_cast<uint32_t *>(a.out + (size_t)t * a.H + hb * 64 + 2 * lane) = lo | (hi << 16);
             keep[hb * 32 + lane] = lo | (hi << 16);
@@ -577,7 +589,9 @@ size_t decode_arrival_words() { return 3 * kArrivalStride; }
 
 cudaError_t decode_setup(const Layer &)
 {
-    return cudaFuncSetAttribute(decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(decode_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    return e;
 }
 
 cudaError_t launch_decode(Layer &L, const uint16_t *x, int T, const uint16_t *residual, const uint16_t *norm_w,
@@ -611,7 +625,7 @@ cudaError_t launch_decode(Layer &L, const uint16_t *x, int T, const uint16_t *re
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, T <= 8 ? decode_kernel<1> : decode_kernel<2>, a);
     *launches += 1;
     return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -30,30 +30,28 @@ struct StreamArgs {
     LinearEpilogue ep;
 };
 
-// Shared memory after the slots: token rows, sums, zeros, per-row exponents, barriers.
+// Shared memory after the slots: token rows, two buffers of sums (the first also a joined tile's), zeros, per-row exponents, barriers.
 struct Layout {
     uint32_t x, sums, zeros, emax, bars, total;
     __host__ __device__ Layout(int T, int KT, int slots) {
         x = (uint32_t)slots * kSlotBytes;
         sums = x + (uint32_t)T * row_bytes(KT);
-        zeros = sums + kMaxTokens * kSumStride * 4;
+        zeros = sums + 2u * T * kSumStride * 4;
         emax = zeros + 256;
         bars = emax + kMaxTokens * 4;
         total = bars + (2 * kMaxSlots + 2) * 8;          // full, empty, rows requested, abort flag
     }
 };
 
-// Outputs of row tile rt from sums[token][row] (per-token factor 2^-sh in inv).
-__device__ __forceinline__ void finish_tile(const StreamArgs &a, int rt, const float *sums, const uint32_t *emax,
-                                            float g0, float g1) {
+// Outputs of row tile rt from its joined sums[token][row].
+__device__ __forceinline__ void finish_tile(const StreamArgs &a, int rt, const float *sums, float g0, float g1) {
     const bool gated = a.ep.act == TFMOE_ACT_SWIGLU;
     const int per = gated ? 64 : 128;
     for (int i = threadIdx.x; i < a.T * per; i += kConsumerThreads) {
         const int t = i / per, j = i % per, n = rt * per + j;
         if (n >= a.ep.N) continue;
-        const float inv = emax ? inverse_up(emax[t]) : 1.f;
         const float *s = sums + t * kSumStride + (gated ? 2 * j : j);
-        store_output(a.ep, t, n, finish_output(a.ep, t, n, s[0] * inv, gated ? s[1] * inv : 0.f, g0, g1));
+        store_output(a.ep, t, n, finish_output(a.ep, t, n, s[0], gated ? s[1] : 0.f, g0, g1));
     }
 }
 
@@ -76,8 +74,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
     ring.abort_flag = reinterpret_cast<volatile int32_t *>(bars + 2 * kMaxSlots + 1);
     const uint32_t requested = ring.full + 8u * (2 * kMaxSlots);
     ring.err_word = a.err_word;
-    const uint32_t G = gridDim.x, c = blockIdx.x, U = (uint32_t)a.RT * a.KT;
-    const uint32_t u0 = first_unit(c, U, G), u1 = first_unit(c + 1, U, G);
+    const uint32_t c = blockIdx.x;
+    const Runs runs((uint32_t)a.RT * a.KT, gridDim.x);
+    const uint32_t u0 = runs.first(c), u1 = runs.first(c + 1);
     const int q0 = (int)(u0 / a.KT), k0 = (int)(u0 - (uint32_t)q0 * a.KT);                   // u0 < u1: G <= U
     const int q1 = (int)((u1 - 1) / a.KT), k1 = (int)(u1 - 1 - (uint32_t)q1 * a.KT) + 1;
     grid_dep_launch_dependents();
@@ -92,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
         }
         fence_mbar_init();
         __syncwarp();
-        asm volatile("bar.arrive 2, %0;" ::"n"(kThreads) : "memory");   // the consumers wait there
+        asm volatile("bar.arrive 10, %0;" ::"n"(kThreads) : "memory");   // the consumers wait there
         if (lane == 0) {
             Cursor cur;
             uint32_t issued = 0;
@@ -112,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
     if (threadIdx.x < 64) reinterpret_cast<uint32_t *>(smem + lay.zeros)[threadIdx.x] = 0;
     const bool gated = a.ep.act == TFMOE_ACT_SWIGLU;
     const float g0 = __ldg(a.ep.global0), g1 = gated ? __ldg(a.ep.global1) : 0.f;
-    asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
+    asm volatile("bar.sync 10, %0;" ::"n"(kThreads) : "memory");
     grid_dep_wait();                                        // before anything another kernel may write
     {
         const bool all = q1 > q0 + 1;
@@ -122,30 +121,41 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
         }, requested);
     }
 
-    const Lane ln;
     uint32_t xa[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int t = 8 * n + (lane >> 2);
         xa[n] = ring.slots + lay.x + (uint32_t)(t < a.T ? t : 0) * row_bytes(a.KT);
     }
-    Cursor cur;
+    Consumer<NT> in(ring);
     Acc<NT> acc;
-    bool cut[2] = {false, false};
+    in.fetch();
+    const bool cut[2] = {k0 > 0 || (q0 == q1 && k1 < a.KT), q1 > q0 && k1 < a.KT};   // the first and the last piece
     for (int q = q0; q <= q1; ++q) {
         const int ka = q == q0 ? k0 : 0, kb = q == q1 ? k1 : a.KT;
         acc.clear();
-        consume_piece<NT>(ring, cur, ln, ka, kb, xa, acc);
-        join_parities<NT>(acc, sums, a.T);
-        if (kb - ka == a.KT) {
-            finish_tile(a, q, sums, emax, g0, g1);
-        } else {
-            cut[q != q0] = true;
+        in.piece(ka, kb, q < q1, xa, true, acc);
+        float *buf = sums + ((q - q0) & 1) * a.T * kSumStride;
+        if (kb - ka < a.KT) {
             float *mine = a.partial + (size_t)(2 * c + (q != q0)) * a.T * 128;
-            for (int i = threadIdx.x; i < a.T * 128; i += kConsumerThreads)
-                mine[i] = sums[(i >> 7) * kSumStride + (i & 127)] * inverse_up(emax[i >> 7]);
+            join_pairs<NT>(acc, buf, a.T, [&](int col, int row, float v) {
+                if (col < a.T) mine[col * 128 + row] = v * inverse_up(emax[col]);
+            });
+        } else if (gated) {
+            join_pairs<NT>(acc, buf, a.T, [&](int col, int row, float v) {
+                const float other = __shfl_xor_sync(0xffffffffu, v, 4);          // the neighbouring row
+                const int n = (q * 128 + row) >> 1;
+                if ((row & 1) || col >= a.T || n >= a.ep.N) return;
+                const float inv = inverse_up(emax[col]);
+                store_output(a.ep, col, n, finish_output(a.ep, col, n, v * inv, other * inv, g0, g1));
+            });
+        } else {
+            join_pairs<NT>(acc, buf, a.T, [&](int col, int row, float v) {
+                const int n = q * 128 + row;
+                if (col < a.T && n < a.ep.N)
+                    store_output(a.ep, col, n, finish_output(a.ep, col, n, v * inverse_up(emax[col]), 0.f, g0, g1));
+            });
         }
-        if (q < q1) consumer_sync();                        // sums are free again
     }
     if (!cut[0] && !cut[1]) return;
     consumer_sync();
@@ -154,11 +164,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
         __threadfence();                                    // the whole CTA's pieces, ordered by the barrier
         if (cut[threadIdx.x]) {
             const uint32_t q = threadIdx.x ? q1 : q0;
-            const uint32_t ca = owner(q * a.KT, U, G), cb = owner((q + 1) * a.KT - 1, U, G);
+            const uint32_t ca = runs.owner(q * a.KT), cb = runs.owner((q + 1) * a.KT - 1);
             is_last = atomicAdd(a.tickets + q, 1) == (int)(cb - ca);
             if (is_last) a.tickets[q] = 0;                  // for the next call
             __threadfence();
-            join[threadIdx.x][1] = (int)(2 * ca + (first_unit(ca, U, G) / a.KT != q));
+            join[threadIdx.x][1] = (int)(2 * ca + (runs.first(ca) / a.KT != q));
             join[threadIdx.x][2] = (int)(2 * cb);
         }
         join[threadIdx.x][0] = is_last;
@@ -189,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
             *reinterpret_cast<float4 *>(sums + (i >> 5) * kSumStride + (i & 31) * 4) = v;
         }
         consumer_sync();
-        finish_tile(a, p ? q1 : q0, sums, nullptr, g0, g1);
+        finish_tile(a, p ? q1 : q0, sums, g0, g1);
         consumer_sync();
     }
 }

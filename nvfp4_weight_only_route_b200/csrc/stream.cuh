@@ -11,19 +11,21 @@
 // One producer lane fills a ring of slots with bulk copies; a slot holds the units of a piece whose
 // column tiles lie in one aligned window of four (two copies: a bulk copy costs the issuing
 // lane about 100 clocks, so small ones would set the pace). 16 consumer warps: warp w takes 16 rows
-// (w mod 8) of pair w / 8 of every window. The product runs on mma.sync m16n8k16 (f16 in, fp32
-// sums), rows of weights against up to 8 tokens per instruction: the tensor core is idle most of
-// the time either way, and this form needs no tensor memory round trip for a few tokens. What has
-// to keep up with HBM (23 bytes = 41 weights per clock and SM) is the decode, one conversion
-// and one scale multiplication per two weights: measured alone, two units take 272 clocks of an SM
-// (8 tokens) or 405 (16 tokens) against 400 at HBM speed. On CUDA cores the products would add an
-// FMA per weight and token.
+// (w mod 8) of pair w / 8 of every window's units; the two warps of a row group add their sums at the
+// end of a piece. (Two groups of 8 warps that take whole pieces in turn need no joining, but leave 8
+// warps to keep up with HBM: the 14-token wide layer took 216 us instead of 188.)
+// The product runs on mma.sync m16n8k16 (f16 in, fp32 sums), rows of weights against up to 8 tokens
+// per instruction: the tensor core is idle most of the time either way, and this form needs no
+// tensor memory round trip for a few tokens. What has to keep up with HBM (23 bytes = 41 weights
+// per clock and SM) is the decode, one conversion (measured: 36 lanes per clock and SM) and one
+// scale multiplication per two weights: a window needs about 570 clocks of an SM's conversions against
+// 800 at HBM speed. On CUDA cores the products would add an FMA per weight and token.
 //
 // The order of the reduction is free, so the lanes read what they can use: lane (g, t) = (l / 4,
-// l % 4) owns rows g and g + 8 and the t-th 32-column half of the pair, four chunks of 8 columns (one
-// word of codes each) in the order t, t + 1, t + 2, t + 3 (mod 4), which puts the 32 lanes on
-// different banks. Chunk i of every lane forms the k indices of two instructions. Token operands
-// are stored in that order too: [128 columns][step 0..3][half 0..3][8 values].
+// l % 4) owns rows g and g + 8 and the t-th 32-column half of a pair of units, four chunks of 8 columns
+// (one word of codes each); step i takes chunk i xor t, which puts the 32 lanes on different banks.
+// The chunks of a step form the k indices of two instructions. Token operands are stored in that
+// order too: [128 columns][step 0..3][half 0..3][8 values].
 #pragma once
 
 #include "common.cuh"
@@ -47,13 +49,27 @@ constexpr int kMaxTokens = 16;                           // two n = 8 tiles
 __host__ __device__ constexpr uint32_t row_bytes(int KT) { return (uint32_t)((KT + 1) / 2) * 256u + 64u; }
 // Byte offset of the 8-value chunk holding column k (a multiple of 8) inside its row.
 __host__ __device__ constexpr uint32_t chunk_offset(int k) {
-    return (uint32_t)(k >> 7) * 256u + (uint32_t)(((k >> 3) - (k >> 5)) & 3) * 64u + (uint32_t)((k >> 5) & 3) * 16u;
+    return (uint32_t)(k >> 7) * 256u + (uint32_t)(((k >> 3) ^ (k >> 5)) & 3) * 64u + (uint32_t)((k >> 5) & 3) * 16u;
 }
 
-// First unit of CTA c, and the CTA that owns unit u, when U units are cut into G runs. The
-// handles keep U below 2^24 and G is the SM count, so the products fit 32 bits.
-__host__ __device__ __forceinline__ uint32_t first_unit(uint32_t c, uint32_t U, uint32_t G) { return c * U / G; }
-__host__ __device__ __forceinline__ uint32_t owner(uint32_t u, uint32_t U, uint32_t G) { return ((u + 1) * G - 1) / U; }
+// U units cut into G runs: the first unit of run c, and the run that holds unit u. The handles keep
+// U below 2^24 and G is at most the SM count, so the products fit 32 bits. A quotient below G is
+// found by one multiplication with the reciprocal (relative error below 2^-22) and a correction.
+struct Runs {
+    uint32_t U, G;
+    float rcp;
+    __device__ __forceinline__ Runs(uint32_t units, uint32_t most) : U(units), G(min(units, most)), rcp(1.0f / (float)units) {}
+    __device__ __forceinline__ uint32_t first(uint32_t c) const { return c * U / G; }
+    __device__ __forceinline__ uint32_t end(uint32_t c) const { return c < G ? first(c + 1) : 0u; }
+    __device__ __forceinline__ uint32_t owner(uint32_t u) const {
+        const uint32_t n = (u + 1) * G - 1;
+        uint32_t q = (uint32_t)((float)n * rcp);
+        const int r = (int)(n - q * U);                    // within +-U: fits
+        if (r < 0) --q;
+        else if ((uint32_t)r >= U) ++q;
+        return q;
+    }
+};
 
 struct Ring {
     uint32_t slots, full, empty;          // shared addresses
@@ -83,9 +99,8 @@ __device__ __forceinline__ bool wait(const Ring &r, uint32_t bar, uint32_t parit
 struct Cursor {
     int slot = 0;
     uint32_t phase = 0;
-    __device__ __forceinline__ void advance(int by, int n) {
-        slot += by;
-        if (slot >= n) { slot -= n; phase ^= 1u; }
+    __device__ __forceinline__ void step(int n) {
+        if (++slot == n) { slot = 0; phase ^= 1u; }
     }
 };
 
@@ -109,7 +124,7 @@ __device__ __forceinline__ bool produce_piece(const Ring &r, Cursor &c, uint32_t
                      ::"r"(full), "r"((uint32_t)n * (kTileCodeBytes + kTileScaleBytes)) : "memory");
         bulk_at(slot + at * kTileCodeBytes, codes + (size_t)k * kTileCodeBytes, n * kTileCodeBytes, full);
         bulk_at(slot + kScaleAt + at * kTileScaleBytes, scales + (size_t)k * kTileScaleBytes, n * kTileScaleBytes, full);
-        c.advance(1, r.n);
+        c.step(r.n);
         ++issued;
         k += n;
     }
@@ -176,8 +191,8 @@ struct Acc {
 struct Lane {
     uint32_t code[4];      // offsets of the lane's four words of row g inside a window's pair, step by step
     uint32_t scale;        // offset of row g's two scale bytes
-    uint32_t sel[2];       // prmt selectors: (scale of step 0, of step 2), (of step 1, of step 3)
-    uint32_t x;            // offset inside 128 columns of a token row
+    uint32_t sel;          // prmt selector: (scale of steps 0 and 1, of steps 2 and 3)
+    uint32_t x;            // offset inside a window's columns of a token row
     int unit;              // the lane's unit of a window
     __device__ __forceinline__ Lane() {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -185,143 +200,168 @@ struct Lane {
         unit = 2 * (warp >> 3) + (t >> 1);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            code[i] = (uint32_t)(unit * kTileCodeBytes + (t & 1) * (kTileCodeBytes / 2) + row * 16 + ((i + t) & 3) * 4);
+            code[i] = (uint32_t)(unit * kTileCodeBytes + (t & 1) * (kTileCodeBytes / 2) + row * 16 + (i ^ t) * 4);
         scale = (uint32_t)(kScaleAt + unit * kTileScaleBytes + row * 4 + (t & 1) * 2);
-        sel[0] = (t >> 1) ? 0x1032u : 0x3210u;               // steps 0 and 2 are in different 16-column blocks,
-        sel[1] = (((1 + t) & 3) >> 1) ? 0x1032u : 0x3210u;   // and so are steps 1 and 3
+        sel = (t >> 1) ? 0x1032u : 0x3210u;                  // steps 0 and 1 are in 16-column block t / 2
         x = (uint32_t)(warp >> 3) * 256u + (uint32_t)t * 16u;
     }
 };
 
-// The codes and scales of the lane's rows of one pair, in registers.
-struct Pair {
-    uint32_t w0[4], w1[4], s0, s1;
-    __device__ __forceinline__ void load(uint32_t slot, const Lane &ln) {
+// A consumer warp's way through the windows of a run of pieces. It always holds the codes of the next
+// window: each word is replaced by the next window's as soon as it is converted, across the pieces'
+// borders too, and the slot is handed back when the last of it is read.
+template <int NT>
+struct Consumer {
+    const Ring &r;
+    Lane ln;
+    Cursor c;
+    uint32_t w0[4], w1[4], s0, s1;     // codes of rows g and g + 8, their scales
+    __device__ __forceinline__ explicit Consumer(const Ring &ring) : r(ring) {}
+
+    __device__ __forceinline__ uint32_t slot() const { return r.slots + (uint32_t)c.slot * kSlotBytes; }
+    __device__ __forceinline__ void release() {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive_at(r.empty + 8u * c.slot);
+        c.step(r.n);
+    }
+    // The first window of a run.
+    __device__ __forceinline__ void fetch() {
+        wait(r, r.full + 8u * c.slot, c.phase);
+        const uint32_t sl = slot();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            w0[i] = lds32(slot + ln.code[i]);
-            w1[i] = lds32(slot + ln.code[i] + 128u);
+            w0[i] = lds32(sl + ln.code[i]);
+            w1[i] = lds32(sl + ln.code[i] + 128u);
         }
-        s0 = lds16(slot + ln.scale);
-        s1 = lds16(slot + ln.scale + 32u);
+        s0 = lds16(sl + ln.scale);
+        s1 = lds16(sl + ln.scale + 32u);
+        release();
+    }
+    // One pair of units against the first N of NT tiles of tokens; x: the lane's operands (token 8 n + g; any
+    // valid row where there is no such token) at the pair's columns. Products E2M1 * E4M3 are exact in
+    // f16 (at most 6 significant bits, 2^-10 to 2688).
+    template <int N, bool Next>
+    __device__ __forceinline__ void multiply(const uint32_t (&x)[NT], uint32_t sa8, uint32_t sb8, Acc<NT> &acc) {
+        uint32_t sl = 0;
+        const uint32_t h0 = __byte_perm(e4m3x2_to_f16x2(sa8), 0, ln.sel), h1 = __byte_perm(e4m3x2_to_f16x2(sb8), 0, ln.sel);
+        const __half2 v0 = *reinterpret_cast<const __half2 *>(&h0), v1 = *reinterpret_cast<const __half2 *>(&h1);
+        if (Next) {
+            wait(r, r.full + 8u * c.slot, c.phase);
+            sl = slot();
+            s0 = lds16(sl + ln.scale);
+            s1 = lds16(sl + ln.scale + 32u);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t a[4], b[4];
+            e2m1x8_to_f16x2x4(w0[i], a);
+            e2m1x8_to_f16x2x4(w1[i], b);
+            if (Next) {
+                w0[i] = lds32(sl + ln.code[i]);
+                w1[i] = lds32(sl + ln.code[i] + 128u);
+            }
+            const __half2 sa = i < 2 ? __low2half2(v0) : __high2half2(v0), sb = i < 2 ? __low2half2(v1) : __high2half2(v1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                a[j] = mul_f16x2(a[j], sa);
+                b[j] = mul_f16x2(b[j], sb);
+            }
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const uint4 xv = lds128(x[n] + 64u * i);
+                mma_f16(acc.c[0][n], a[0], b[0], a[1], b[1], xv.x, xv.y);
+                mma_f16(acc.c[1][n], a[2], b[2], a[3], b[3], xv.z, xv.w);
+            }
+        }
+        if (Next) release();
+    }
+    // One piece, the column tiles [ka, kb) of a row tile, whose first window is held; `more`: another
+    // piece follows, whose first window is held afterwards. xa: the lane's token rows; `two`: the
+    // second tile of tokens has some.
+    __device__ __forceinline__ void piece(int ka, int kb, bool more, const uint32_t (&xa)[NT], bool two, Acc<NT> &acc) {
+        uint32_t x[NT];
+        int w = ka & ~(kWindow - 1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[n] = xa[n] + ln.x + (uint32_t)w * 128u;
+        for (; w < kb; w += kWindow) {
+            uint32_t xl[NT];
+            uint32_t sa = s0, sb = s1;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) xl[n] = x[n];
+            if (w < ka || w + kWindow > kb) {
+                // only some of the window's units: a lane without a unit multiplies zeros by zero scales (zero times
+                // what an earlier window or an infinite activation left there could be a NaN)
+                if (w + ln.unit < ka || w + ln.unit >= kb) {
+                    sa = sb = 0u;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) xl[n] = r.zeros;
+                }
+            }
+            if (more || w + kWindow < kb) {
+                if (NT == 1 || !two) multiply<1, true>(xl, sa, sb, acc);
+                else multiply<NT, true>(xl, sa, sb, acc);
+            } else {
+                multiply<NT, false>(xl, sa, sb, acc);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) x[n] += kWindow * 128u;
+        }
     }
 };
 
-// One pair of a window. x: the lane's operands (token 8 n + g; any valid row where there is no such
-// token) at the pair's columns. Products E2M1 * E4M3 are exact in f16 (at most 6 significant
-// bits, 2^-10 to 2688).
-template <int NT>
-__device__ __forceinline__ void consume_pair(const Pair &p, const Lane &ln, const uint32_t (&x)[NT], Acc<NT> &acc) {
-    const uint32_t h0 = e4m3x2_to_f16x2(p.s0), h1 = e4m3x2_to_f16x2(p.s1);
-    __half2 v0[2], v1[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const uint32_t a = __byte_perm(h0, 0, ln.sel[j]), b = __byte_perm(h1, 0, ln.sel[j]);
-        v0[j] = *reinterpret_cast<const __half2 *>(&a);
-        v1[j] = *reinterpret_cast<const __half2 *>(&b);
+// The pieces of a run [u, end) of units, row tile after row tile: ka..kb of row tile rt (of RT) of expert
+// ei. Stepping takes no division.
+struct Pieces {
+    uint32_t u, end;
+    int RT, KT, ei, rt, ka, kb;
+    __device__ __forceinline__ Pieces(uint32_t first, uint32_t last, int row_tiles, int col_tiles)
+        : u(first), end(last), RT(row_tiles), KT(col_tiles) {
+        const uint32_t q = u / (uint32_t)KT;
+        ei = (int)(q / (uint32_t)RT);
+        rt = (int)(q - (uint32_t)ei * RT);
+        ka = (int)(u - q * KT);
+        kb = (int)min((uint32_t)KT, ka + (end - u));
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t a[4], b[4];
-        e2m1x8_to_f16x2x4(p.w0[i], a);
-        e2m1x8_to_f16x2x4(p.w1[i], b);
-        const __half2 sa = i < 2 ? __low2half2(v0[i & 1]) : __high2half2(v0[i & 1]);
-        const __half2 sb = i < 2 ? __low2half2(v1[i & 1]) : __high2half2(v1[i & 1]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            a[j] = mul_f16x2(a[j], sa);
-            b[j] = mul_f16x2(b[j], sb);
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const uint4 xv = lds128(x[n] + 64u * i);
-            mma_f16(acc.c[0][n], a[0], b[0], a[1], b[1], xv.x, xv.y);
-            mma_f16(acc.c[1][n], a[2], b[2], a[3], b[3], xv.z, xv.w);
-        }
+    __device__ __forceinline__ bool valid() const { return u < end; }
+    __device__ __forceinline__ bool more() const { return u + (kb - ka) < end; }
+    __device__ __forceinline__ void next() {
+        u += kb - ka;
+        if (++rt == RT) { rt = 0; ++ei; }
+        ka = 0;
+        kb = (int)min((uint32_t)KT, end - u);
     }
-}
-
-// One piece, the column tiles [ka, kb) of a row tile: this warp's share of its windows. xa: the
-// lane's token rows. Whole windows run two at a time: the next one's codes are read (and its slot
-// handed back) before the current one is multiplied.
-template <int NT>
-__device__ __forceinline__ void consume_piece(const Ring &r, Cursor &c, const Lane &ln, int ka, int kb,
-                                              const uint32_t (&xa)[NT], Acc<NT> &acc) {
-    const int lane = threadIdx.x & 31;
-    int w = ka & ~(kWindow - 1);
-    uint32_t x[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) x[n] = xa[n] + ln.x + (uint32_t)w * 128u;
-    auto step = [&]() {
-        w += kWindow;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) x[n] += kWindow * 128u;
-    };
-    auto fetch = [&](Pair &p) {
-        wait(r, r.full + 8u * c.slot, c.phase);
-        p.load(r.slots + (uint32_t)c.slot * kSlotBytes, ln);
-        __syncwarp();
-        if (lane == 0) mbar_arrive_at(r.empty + 8u * c.slot);
-        c.advance(1, r.n);
-    };
-    // a window of which the piece has only some units: a lane without a unit multiplies zeros by zero
-    // scales (zero times what an earlier window or an infinite activation left there could be a NaN)
-    auto part = [&]() {
-        Pair p;
-        fetch(p);
-        const bool live = w + ln.unit >= ka && w + ln.unit < kb;
-        if (!live) p.s0 = p.s1 = 0u;
-        uint32_t xl[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) xl[n] = live ? x[n] : r.zeros;
-        if (__any_sync(0xffffffffu, live)) consume_pair<NT>(p, ln, xl, acc);
-        step();
-    };
-    if (w < ka || w + kWindow > kb) part();
-    int whole = (kb - w) / kWindow;
-    if (whole > 0) {
-        Pair p0, p1;
-        fetch(p0);
-        for (; whole >= 2; whole -= 2) {
-            fetch(p1);
-            consume_pair<NT>(p0, ln, x, acc);
-            step();
-            if (whole > 2) fetch(p0);
-            consume_pair<NT>(p1, ln, x, acc);
-            step();
-        }
-        if (whole) {
-            consume_pair<NT>(p0, ln, x, acc);
-            step();
-        }
-    }
-    if (w < kb) part();
-}
+};
 
 // Barrier among the consumer warps.
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumerThreads) : "memory"); }
 
-// Add the two parities' sums of a piece: sums[token][row] (stride kSumStride floats) for `m`
-// tokens. Ends with a consumer barrier, after which every consumer may read it; the next call
-// must come after another barrier.
+// The sums of a finished piece: warps 8 to 15 hand theirs to warps 0 to 7 through `buf` ([column][128
+// rows], kSumStride floats a column), and those call f(column, row of the tile, sum) for their values of
+// the first m columns, every lane of a warp in each call. The two warps of a row group meet at a barrier of
+// their own; two buffers in turn make it one meeting per piece.
 constexpr int kSumStride = 132;
-template <int NT>
-__device__ __forceinline__ void join_parities(const Acc<NT> &acc, float *sums, int m) {
+template <int NT, class F>
+__device__ __forceinline__ void join_pairs(const Acc<NT> &acc, float *buf, int m, F f) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int row = (warp & 7) * 16 + g;
-    for (int par = 1; par >= 0; --par) {
-        if ((warp >> 3) == par) {
+    float *mine = buf + 2 * t * kSumStride + (warp & 7) * 16 + g;
+    if (warp >= 8) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int col = 8 * n + 2 * t + (j & 1);
-                    if (col >= m) continue;
-                    float *p = sums + col * kSumStride + row + 8 * (j >> 1);
-                    *p = par ? acc.sum(n, j) : *p + acc.sum(n, j);
-                }
-        }
-        consumer_sync();
+            for (int j = 0; j < 4; ++j)
+                if (8 * n + 2 * t + (j & 1) < m) mine[(8 * n + (j & 1)) * kSumStride + 8 * (j >> 1)] = acc.sum(n, j);
+    }
+    asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 7)) : "memory");
+    if (warp < 8) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (8 * n + (j & 1) >= m) continue;          // no lane has a column below m
+                const int col = 8 * n + 2 * t + (j & 1);
+                const float other = col < m ? mine[(8 * n + (j & 1)) * kSumStride + 8 * (j >> 1)] : 0.f;
+                f(col, (warp & 7) * 16 + g + 8 * (j >> 1), acc.sum(n, j) + other);
+            }
     }
 }
 
@@ -369,19 +409,22 @@ __device__ __forceinline__ void convert_rows(const uint16_t *x, int64_t ld, uint
     while (tpr * T > kConsumerThreads) tpr >>= 1;
     const int t = threadIdx.x / tpr, i0 = threadIdx.x % tpr;
     const uint4 *row = reinterpret_cast<const uint4 *>(x + (int64_t)t * ld);
+    const int rounds = (chunks + tpr - 1) / tpr;
     uint4 v[kHeld];
     if (t < T) {
 #pragma unroll
         for (int j = 0; j < kHeld; ++j) {
             const int i = i0 + j * tpr;
-            v[j] = i * 8 < K && used(i >> 4) ? row[i] : make_uint4(0, 0, 0, 0);
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (j < rounds && i * 8 < K && used(i >> 4)) v[j] = row[i];
         }
     }
     if (requested && (threadIdx.x & 31) == 0) mbar_arrive_at(requested);
     if (t < T) {
         uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < kHeld; ++j) m = max_bits(v[j], m);
+        for (int j = 0; j < kHeld; ++j)
+            if (j < rounds) m = max_bits(v[j], m);
 #pragma unroll 4
         for (int i = i0 + kHeld * tpr; i * 8 < K; i += tpr)
             if (used(i >> 4)) m = max_bits(row[i], m);
@@ -395,6 +438,7 @@ __device__ __forceinline__ void convert_rows(const uint16_t *x, int64_t ld, uint
 #pragma unroll
         for (int j = 0; j < kHeld; ++j) {
             const int i = i0 + j * tpr;
+            if (j >= rounds) break;
             if (i < chunks && used(i >> 4)) *reinterpret_cast<uint4 *>(dst + chunk_offset(i * 8)) = bf16x8_to_f16(v[j], up);
         }
 #pragma unroll 4

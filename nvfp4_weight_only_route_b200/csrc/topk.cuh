@@ -17,59 +17,76 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// One warp selects a token's top k experts: k rounds, each a lane-local best (largest key,
-// lowest expert on ties) followed by a warp-wide max of the keys and a min of the expert ids
-// that hold it (two redux.sync), so ties go to the lower expert index. With m shared slots the
-// row continues with slots k..k+m-1 = experts E..E+m-1 at weight 1 (the shared expert).
+// The logit of a key (+0 for a zero of either sign).
+__device__ __forceinline__ float logit_of_key(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
+// The top k experts of one token by one warp: lane s < k ends with the s-th expert's id and its softmax
+// weight over the k selected logits. Each lane keeps its best remaining expert (largest key, lower
+// expert on ties); a round takes the warp's largest key and the lowest expert that holds it (two
+// redux.sync), so ties go to the lower expert index, and only the winner's lane searches its next best.
+template <int kMaxEPerLane>
+__device__ __forceinline__ void topk_lanes(const float *row, int E, int k, int &my_id, float &my_w)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t key[kMaxEPerLane];
+    uint32_t left = 0;                        // bit i: candidate lane + 32 i remains
+#pragma unroll
+    for (int i = 0; i < kMaxEPerLane; ++i) {
+        const int e = lane + 32 * i;
+        const bool in = e < E;
+        key[i] = in ? logit_key(__ldcg(row + e)) : 0u;
+        left |= in ? 1u << i : 0u;
+    }
+    uint32_t best_key = 0u, best_id = 0xffffffffu;
+    auto search = [&]() {
+        best_key = 0u;
+        best_id = 0xffffffffu;
+#pragma unroll
+        for (int i = kMaxEPerLane - 1; i >= 0; --i)       // downwards: the lower expert keeps ties
+            if ((left & (1u << i)) && key[i] >= best_key) {
+                best_key = key[i];
+                best_id = (uint32_t)(lane + 32 * i);
+            }
+    };
+    search();
+    uint32_t first = 0u, mine = 0u;
+    my_id = -1;
+    for (int s = 0; s < k; ++s) {
+        const uint32_t mk = __reduce_max_sync(0xffffffffu, best_key);
+        const uint32_t win = __reduce_min_sync(0xffffffffu, best_key == mk ? best_id : 0xffffffffu);
+        if (s == 0) first = mk;
+        if (lane == s) { mine = mk; my_id = (int)win; }
+        if (best_id == win) {
+            left &= ~(1u << (win >> 5));
+            search();
+        }
+    }
+    const float ex = (lane < k) ? expf(logit_of_key(mine) - logit_of_key(first)) : 0.f;
+    float den = ex;
+    for (int o = k <= 8 ? 4 : 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);   // lanes from k on hold 0
+    my_w = ex / den;
+}
+__device__ __forceinline__ void topk_select(const float *row, int E, int k, int &my_id, float &my_w) {
+    if (E <= 128) topk_lanes<4>(row, E, k, my_id, my_w);
+    else topk_lanes<kMaxEPerLane>(row, E, k, my_id, my_w);
+}
+
+// As topk_select, into the token's rows of ids and weights. With m shared slots the rows continue with
+// slots k..k+m-1 = experts E..E+m-1 at weight 1 (the shared expert).
 __device__ __forceinline__ void topk_warp(const float *row, int E, int k, int32_t *ids_row, float *w_row,
                                           int32_t *ids_copy = nullptr, int m = 0)
 {
     const int lane = threadIdx.x & 31;
-    float v[kMaxEPerLane];
-    uint32_t key[kMaxEPerLane];
-    uint32_t taken = 0;                       // bit i: candidate lane + 32 i used or absent
-#pragma unroll
-    for (int i = 0; i < kMaxEPerLane; ++i) {
-        const int e = lane + 32 * i;
-        v[i] = (e < E) ? __ldcg(row + e) : 0.f;
-        key[i] = logit_key(v[i]);
-        if (e >= E) taken |= 1u << i;
-    }
-    float sel_first = 0.f, my_sel = 0.f;
-    int my_id = -1;
-    for (int s = 0; s < k; ++s) {
-        uint32_t bk = 0u;
-        float bv = 0.f;
-#pragma unroll
-        for (int i = 0; i < kMaxEPerLane; ++i) {
-            if (!(taken & (1u << i)) && key[i] > bk) {   // strict: the lower i (lower expert) keeps ties
-                bk = key[i];
-                bv = v[i];
-            }
-        }
-        const uint32_t mk = __reduce_max_sync(0xffffffffu, bk);
-        uint32_t mine = 0xffffffffu;
-#pragma unroll
-        for (int i = kMaxEPerLane - 1; i >= 0; --i)
-            if (!(taken & (1u << i)) && key[i] == mk) mine = (uint32_t)(lane + 32 * i);
-        const uint32_t win = __reduce_min_sync(0xffffffffu, mine);
-        const float wv = __shfl_sync(0xffffffffu, bv, (int)(win & 31u));
-        if ((int)(win & 31u) == lane) taken |= 1u << (win >> 5);
-        if (s == 0) sel_first = wv;
-        if (lane == s) { my_sel = wv; my_id = (int)win; }
-    }
-    const float ex = (lane < k) ? expf(my_sel - sel_first) : 0.f;
-    float den = ex;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-    if (lane < k) {
-        ids_row[lane] = my_id;
-        w_row[lane] = ex / den;
-        if (ids_copy) ids_copy[lane] = my_id;
-    } else if (lane < k + m) {
-        ids_row[lane] = E + lane - k;
-        w_row[lane] = 1.f;
-        if (ids_copy) ids_copy[lane] = E + lane - k;
+    int id;
+    float w;
+    topk_select(row, E, k, id, w);
+    if (lane >= k) { id = E + lane - k; w = 1.f; }
+    if (lane < k + m) {
+        ids_row[lane] = id;
+        w_row[lane] = w;
+        if (ids_copy) ids_copy[lane] = id;
     }
 }
 

@@ -160,6 +160,7 @@ def _check(oracle_mod, layer, shape, x, got, m=0, residual=None, norm_w=None, ep
     (2048, 768, 128, 8, 0, 8),
     (1024, 2688, 16, 4, 0, 5),
     (256, 64, 250, 26, 6, 16),    # 32 slots per token, 512 pairs
+    (4096, 384, 56, 8, 0, 14),    # long row tiles, several per SM, in the short ring of long token rows
 ])
 def test_shapes(oracle_mod, H, I, E, k, m, T):
     shape, layer = _layer(H, I, E, k, m, seed=70 + T)

@@ -113,6 +113,11 @@ def test_long_reduction_beyond_the_streaming_operands():
     _case(1, 65536, 130, fp32=True)
 
 
+def test_long_pieces_in_a_short_ring():
+    """Row tiles of 64 column tiles, several per SM, with the ring of sixteen long token rows."""
+    _case(16, 4096, 24000, fp32=True)
+
+
 def test_wide_output_of_one_token():
     _case(1, 64, 40000, fp32=True)
 
