@@ -243,22 +243,6 @@ __device__ void make_plan(const DecodeArgs &a, Plan &pl) {
     consumer_sync();
 }
 
-// One piece through the consumers: the sums of m columns, times factor(column), to dst [m][128].
-template <int NT, class RowOf, class Factor>
-__device__ __forceinline__ void run_piece(Consumer<NT> &in, const Pieces &p, int m, RowOf row_of, Factor factor, float *buf,
-                                          float *dst) {
-    const int g = (threadIdx.x & 31) >> 2;
-    uint32_t xa[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) xa[n] = row_of(8 * n + g < m ? 8 * n + g : 0);
-    Acc<NT> acc;
-    acc.clear();
-    in.piece(p.ka, p.kb, p.more(), xa, m > 8, acc);
-    join_pairs<NT>(acc, buf, m, [&](int col, int row, float v) {
-        if (col < m) dst[col * 128 + row] = v * factor(col);
-    });
-}
-
 // a = silu(G) U of the plan's rows [ra, rb) as operand rows 0, 1, ..., from the gate/up pieces.
 __device__ void prepare_a(const DecodeArgs &a, const Plan &pl, int ra, int rb, const Runs &r1, uint8_t *rows, uint32_t *emax) {
     const int RT = a.I / 64, KT = a.H / kTileK, KT2 = a.I / kTileK, half = a.I / 2;
@@ -394,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
     const int KT1 = a.H / kTileK, RT1 = a.I / 64, KT2 = a.I / kTileK, RT2 = a.H / kTileRows;
     const Layout lay(a.T, KT1, KT2, a.slots);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + lay.bars);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t G = gridDim.x, c = blockIdx.x;
     Ring ring;
     ring.slots = smem_u32(smem);
@@ -422,8 +406,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
     if (threadIdx.x < 64) reinterpret_cast<uint32_t *>(smem + lay.zeros)[threadIdx.x] = 0;
     __syncthreads();
 
-    if (warp == kConsumers) {
-        if (lane == 0 && wait(ring, planned, 0)) {
+    if (warp >= kConsumers) {
+        give_registers();
+        if (warp == kConsumers && lane == 0 && wait(ring, planned, 0)) {
             Cursor cur;
             uint32_t issued = 0;
             bool ok = true;
@@ -443,9 +428,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
         return;
     }
 
+    take_registers();
     uint32_t *emax = reinterpret_cast<uint32_t *>(smem + lay.emax);
     uint8_t *rows = smem + lay.rows;
-    float *sums = reinterpret_cast<float *>(smem + lay.sums);
     uint32_t *arrive0 = a.arrivals, *arrive1 = a.arrivals + kArrivalStride, *arrive2 = a.arrivals + 2 * kArrivalStride;
 
     router_logits(a, part);
@@ -466,49 +451,71 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
     make_plan(a, pl);
     if (threadIdx.x == 0) mbar_arrive_at(planned);
 
+    // gate/up, then down: one loop, so that both run the same code
     Consumer<NT> in(ring);
-    int turn = 0;                                        // which buffer of sums
-    const Runs r1 = runs_of(pl.n_act * RT1 * KT1, G), r2 = runs_of(pl.n_act * RT2 * KT2, G);
+    float *buf = reinterpret_cast<float *>(smem + lay.sums), *other = buf + a.T * kSumStride;   // of sums, in turn
+    const int n_act = uniform(pl.n_act);
+    const Runs r1 = runs_of(n_act * RT1 * KT1, G), r2 = runs_of(n_act * RT2 * KT2, G);
     const uint32_t rows_at = ring.slots + lay.rows;
-    {
-        const uint32_t rb = row_bytes(KT1);
-        Pieces p(r1.first(c), r1.end(c), RT1, KT1);
-        if (p.valid()) in.fetch();
-        for (; p.valid(); p.next()) {
-            const int m = pl.cnt[p.ei], poff = pl.poff[p.ei];
-            run_piece<NT>(in, p, m, [&](int col) { return rows_at + pl.tok[poff + col] * rb; },
-                          [&](int col) { return inverse_up(emax[pl.tok[poff + col]]); }, sums + turn * a.T * kSumStride,
-                          a.gu_part + piece_at(poff, RT1, p.rt, m, c, a.T));
-            turn ^= 1;
+    const int g = lane >> 2, t = lane & 3;
+    // the a rows of as many of the down run's experts as fit are prepared together: rows [r0, r_end)
+    const int fit = (int)((uint32_t)a.T * row_bytes(KT1 > KT2 ? KT1 : KT2) / row_bytes(KT2));
+    int r0 = 0, r_end = 0;
+#pragma unroll 1
+    for (int down = 0; down < 2; ++down) {
+        if (down) {
+            grid_arrive(arrive1);
+            grid_wait(ring, arrive1, G);
+            if (c == 0 && threadIdx.x == 0) *arrive0 = 0;
         }
-    }
-    grid_arrive(arrive1);
-    grid_wait(ring, arrive1, G);
-    if (c == 0 && threadIdx.x == 0) *arrive0 = 0;
-    {
-        const uint32_t rb = row_bytes(KT2);
-        // the rows of as many of the run's experts as fit are prepared together
-        const int fit = (int)((uint32_t)a.T * row_bytes(KT1 > KT2 ? KT1 : KT2) / rb);
-        int r0 = 0, r_end = 0;
-        uint32_t *ea = emax + kMaxTokens;
-        Pieces p(r2.first(c), r2.end(c), RT2, KT2);
+        const int RT = down ? RT2 : RT1, KT = down ? KT2 : KT1;
+        const uint32_t rb = row_bytes(KT);
+        const uint32_t *em = down ? emax + kMaxTokens : emax;
+        Pieces p(down ? r2.first(c) : r1.first(c), down ? r2.end(c) : r1.end(c), RT, KT);
         if (p.valid()) in.fetch();
-        for (; p.valid(); p.next()) {
-            const int m = pl.cnt[p.ei], poff = pl.poff[p.ei];
-            if (poff >= r_end) {
-                const int last = (int)((p.end - 1) / ((uint32_t)RT2 * KT2));
-                int el = p.ei;
-                while (el < last && pl.poff[el + 1] + pl.cnt[el + 1] - poff <= fit) ++el;
-                r0 = poff;
-                r_end = pl.poff[el] + pl.cnt[el];
-                consumer_sync();                         // the rows in use are free
-                prepare_a(a, pl, r0, r_end, r1, rows, ea);
+        while (p.valid()) {
+            const int ei = p.ei, m = uniform(pl.cnt[ei]), poff = uniform(pl.poff[ei]);
+            float scale = 1.f;
+            if (down) {
+                if (poff >= r_end) {
+                    const int last = (int)((p.end - 1) / ((uint32_t)RT2 * KT2));
+                    int el = ei;
+                    while (el < last && pl.poff[el + 1] + pl.cnt[el + 1] - poff <= fit) ++el;
+                    r0 = poff;
+                    r_end = uniform(pl.poff[el] + pl.cnt[el]);
+                    consumer_sync();                     // the rows in use are free
+                    prepare_a(a, pl, r0, r_end, r1, rows, emax + kMaxTokens);
+                }
+                scale = __ldg(a.down_global + pl.list[ei]);
             }
-            const float dg = __ldg(a.down_global + pl.list[p.ei]);
-            run_piece<NT>(in, p, m, [&](int col) { return rows_at + (uint32_t)(poff - r0 + col) * rb; },
-                          [&](int col) { return inverse_up(ea[poff - r0 + col]) * dg; }, sums + turn * a.T * kSumStride,
-                          a.d_part + piece_at(poff, RT2, p.rt, m, c, a.T));
-            turn ^= 1;
+            // the lane's operand rows and the factors of its sums: columns are the expert's tokens
+            uint32_t xa[NT];
+            float f[NT][2];
+            auto row = [&](int col) { return (uint32_t)(down ? poff - r0 + col : pl.tok[poff + col]); };
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                xa[n] = rows_at + row(8 * n + g < m ? 8 * n + g : 0) * rb;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int col = 8 * n + 2 * t + j;
+                    f[n][j] = col < m ? inverse_up(em[row(col)]) * scale : 0.f;
+                }
+            }
+            float *dst = (down ? a.d_part : a.gu_part) + piece_at(poff, RT, p.rt, m, c, a.T) + (2 * t) * 128 + (warp & 7) * 16 + g;
+            const bool two = m > 8;
+            do {
+                Acc<NT> acc;
+                acc.clear();
+                in.piece(p.ka, p.kb, p.more(), xa, two, acc);
+                join_pairs<NT>(acc, buf, m, [&](int n, int j, float v) {
+                    if (8 * n + 2 * t + (j & 1) < m) dst[(8 * n + (j & 1)) * 128 + 8 * (j >> 1)] = v * f[n][j & 1];
+                });
+                float *const swap = buf;
+                buf = other;
+                other = swap;
+                dst += m * 128;                          // the next tile's columns follow this one's
+                p.next();
+            } while (p.valid() && p.ei == ei);
         }
     }
     grid_arrive(arrive2);

@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
     float *sums = reinterpret_cast<float *>(smem + lay.sums);
     uint32_t *emax = reinterpret_cast<uint32_t *>(smem + lay.emax);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + lay.bars);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     Ring ring;
     ring.slots = smem_u32(smem);
     ring.full = smem_u32(bars);
@@ -80,7 +80,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
     const int q0 = (int)(u0 / a.KT), k0 = (int)(u0 - (uint32_t)q0 * a.KT);                   // u0 < u1: G <= U
     const int q1 = (int)((u1 - 1) / a.KT), k1 = (int)(u1 - 1 - (uint32_t)q1 * a.KT) + 1;
     grid_dep_launch_dependents();
-    if (warp == kConsumers) {
+    if (warp >= kConsumers) {
+        give_registers();
+        if (warp > kConsumers) return;
         if (lane < a.slots) {
             mbar_init(bars + lane, 1);
             mbar_init(bars + kMaxSlots + lane, kConsumers);
@@ -91,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
         }
         fence_mbar_init();
         __syncwarp();
-        asm volatile("bar.arrive 10, %0;" ::"n"(kThreads) : "memory");   // the consumers wait there
+        asm volatile("bar.arrive 10, %0;" ::"n"(kConsumerThreads + 32) : "memory");   // the consumers wait there
         if (lane == 0) {
             Cursor cur;
             uint32_t issued = 0;
@@ -107,11 +109,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
         return;
     }
 
+    take_registers();
     if (threadIdx.x < kMaxTokens) emax[threadIdx.x] = 0;
     if (threadIdx.x < 64) reinterpret_cast<uint32_t *>(smem + lay.zeros)[threadIdx.x] = 0;
     const bool gated = a.ep.act == TFMOE_ACT_SWIGLU;
     const float g0 = __ldg(a.ep.global0), g1 = gated ? __ldg(a.ep.global1) : 0.f;
-    asm volatile("bar.sync 10, %0;" ::"n"(kThreads) : "memory");
+    asm volatile("bar.sync 10, %0;" ::"n"(kConsumerThreads + 32) : "memory");
     grid_dep_wait();                                        // before anything another kernel may write
     {
         const bool all = q1 > q0 + 1;
@@ -136,13 +139,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
         acc.clear();
         in.piece(ka, kb, q < q1, xa, true, acc);
         float *buf = sums + ((q - q0) & 1) * a.T * kSumStride;
+        const int row0 = (warp & 7) * 16 + (lane >> 2), col0 = 2 * (lane & 3);
         if (kb - ka < a.KT) {
             float *mine = a.partial + (size_t)(2 * c + (q != q0)) * a.T * 128;
-            join_pairs<NT>(acc, buf, a.T, [&](int col, int row, float v) {
+            join_pairs<NT>(acc, buf, a.T, [&](int i, int j, float v) {
+                const int col = 8 * i + col0 + (j & 1), row = row0 + 8 * (j >> 1);
                 if (col < a.T) mine[col * 128 + row] = v * inverse_up(emax[col]);
             });
         } else if (gated) {
-            join_pairs<NT>(acc, buf, a.T, [&](int col, int row, float v) {
+            join_pairs<NT>(acc, buf, a.T, [&](int i, int j, float v) {
+                const int col = 8 * i + col0 + (j & 1), row = row0 + 8 * (j >> 1);
                 const float other = __shfl_xor_sync(0xffffffffu, v, 4);          // the neighbouring row
                 const int n = (q * 128 + row) >> 1;
                 if ((row & 1) || col >= a.T || n >= a.ep.N) return;
@@ -150,7 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
                 store_output(a.ep, col, n, finish_output(a.ep, col, n, v * inv, other * inv, g0, g1));
             });
         } else {
-            join_pairs<NT>(acc, buf, a.T, [&](int col, int row, float v) {
+            join_pairs<NT>(acc, buf, a.T, [&](int i, int j, float v) {
+                const int col = 8 * i + col0 + (j & 1), row = row0 + 8 * (j >> 1);
                 const int n = q * 128 + row;
                 if (col < a.T && n < a.ep.N)
                     store_output(a.ep, col, n, finish_output(a.ep, col, n, v * inverse_up(emax[col]), 0.f, g0, g1));

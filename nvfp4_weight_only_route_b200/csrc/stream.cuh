@@ -36,7 +36,13 @@ namespace stream {
 
 constexpr int kConsumers = 16;                           // warps
 constexpr int kConsumerThreads = 32 * kConsumers;
-constexpr int kThreads = kConsumerThreads + 32;          // + the producer warp
+constexpr int kThreads = kConsumerThreads + 128;         // + the producer's warpgroup, of which one lane works
+// A scheduler's four consumer warps and its share of the producer's group: 640 threads start with 96
+// registers each (61440 in all); the consumers take 112, the producer's warps keep 24 (60416).
+constexpr int kConsumerRegs = 112, kProducerRegs = 24;
+static_assert(kConsumerThreads * kConsumerRegs + 128 * kProducerRegs <= kThreads * 96, "register split");
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs)); }
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs)); }
 constexpr int kWindow = 4;                               // column tiles per slot
 constexpr int kScaleAt = kWindow * kTileCodeBytes;       // 16384
 constexpr int kSlotBytes = kScaleAt + kWindow * kTileScaleBytes;   // 18432
@@ -94,6 +100,18 @@ __device__ __forceinline__ bool wait(const Ring &r, uint32_t bar, uint32_t parit
         }
     }
 }
+
+// The same by a whole warp, which goes on together.
+__device__ __forceinline__ void wait_warp(const Ring &r, uint32_t bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_at(bar, parity))) return;
+    wait(r, bar, parity);
+    __syncwarp();
+}
+
+// A value that is the same in every lane, in a form the compiler takes as such: loops and branches on
+// values from shared memory are otherwise compiled for lanes that may part, which slowed the
+// product's loop by half.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // Slot and phase of a running group number, advanced without dividing.
 struct Cursor {
@@ -194,16 +212,20 @@ struct Lane {
     uint32_t sel;          // prmt selector: (scale of steps 0 and 1, of steps 2 and 3)
     uint32_t x;            // offset inside a window's columns of a token row
     int unit;              // the lane's unit of a window
+    bool first;            // lane 0
     __device__ __forceinline__ Lane() {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         const int row = (warp & 7) * 16 + g;
         unit = 2 * (warp >> 3) + (t >> 1);
+        first = lane == 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             code[i] = (uint32_t)(unit * kTileCodeBytes + (t & 1) * (kTileCodeBytes / 2) + row * 16 + (i ^ t) * 4);
         scale = (uint32_t)(kScaleAt + unit * kTileScaleBytes + row * 4 + (t & 1) * 2);
         sel = (t >> 1) ? 0x1032u : 0x3210u;                  // steps 0 and 1 are in 16-column block t / 2
         x = (uint32_t)(warp >> 3) * 256u + (uint32_t)t * 16u;
+        // kept in registers, not worked out anew in every window
+        asm volatile("" : "+r"(code[0]), "+r"(code[1]), "+r"(code[2]), "+r"(code[3]), "+r"(scale), "+r"(sel), "+r"(x));
     }
 };
 
@@ -214,57 +236,59 @@ template <int NT>
 struct Consumer {
     const Ring &r;
     Lane ln;
-    Cursor c;
+    uint32_t slot, bar, phase;         // the slot to read next, its full barrier, its phase
+    uint32_t end;                      // one past the last full barrier
     uint32_t w0[4], w1[4], s0, s1;     // codes of rows g and g + 8, their scales
-    __device__ __forceinline__ explicit Consumer(const Ring &ring) : r(ring) {}
+    __device__ __forceinline__ explicit Consumer(const Ring &ring)
+        : r(ring), slot(ring.slots), bar(ring.full), phase(0), end(ring.full + 8u * ring.n) {}
 
-    __device__ __forceinline__ uint32_t slot() const { return r.slots + (uint32_t)c.slot * kSlotBytes; }
     __device__ __forceinline__ void release() {
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive_at(r.empty + 8u * c.slot);
-        c.step(r.n);
+        if (ln.first) mbar_arrive_at(bar + 8u * kMaxSlots);
+        slot += kSlotBytes;
+        bar += 8u;
+        if (bar == end) {
+            slot = r.slots;
+            bar = r.full;
+            phase ^= 1u;
+        }
     }
     // The first window of a run.
     __device__ __forceinline__ void fetch() {
-        wait(r, r.full + 8u * c.slot, c.phase);
-        const uint32_t sl = slot();
+        wait_warp(r, bar, phase);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            w0[i] = lds32(sl + ln.code[i]);
-            w1[i] = lds32(sl + ln.code[i] + 128u);
+            w0[i] = lds32(slot + ln.code[i]);
+            w1[i] = lds32(slot + ln.code[i] + 128u);
         }
-        s0 = lds16(sl + ln.scale);
-        s1 = lds16(sl + ln.scale + 32u);
+        s0 = lds16(slot + ln.scale);
+        s1 = lds16(slot + ln.scale + 32u);
         release();
     }
-    // One pair of units against the first N of NT tiles of tokens; x: the lane's operands (token 8 n + g; any
-    // valid row where there is no such token) at the pair's columns. Products E2M1 * E4M3 are exact in
-    // f16 (at most 6 significant bits, 2^-10 to 2688).
-    template <int N, bool Next>
-    __device__ __forceinline__ void multiply(const uint32_t (&x)[NT], uint32_t sa8, uint32_t sb8, Acc<NT> &acc) {
-        uint32_t sl = 0;
-        const uint32_t h0 = __byte_perm(e4m3x2_to_f16x2(sa8), 0, ln.sel), h1 = __byte_perm(e4m3x2_to_f16x2(sb8), 0, ln.sel);
+    // One pair of units, with scales sa and sb, against the first N of NT tiles of tokens; x: the lane's
+    // operands (token 8 n + g; any valid row where there is no such token) at the pair's columns. `next`:
+    // fetch the next window's. Products E2M1 * E4M3 are exact in f16 (at most 6 significant bits,
+    // 2^-10 to 2688).
+    template <int N>
+    __device__ __forceinline__ void multiply(const uint32_t (&x)[NT], uint32_t sa, uint32_t sb, bool next, Acc<NT> &acc) {
+        const uint32_t h0 = __byte_perm(e4m3x2_to_f16x2(sa), 0, ln.sel), h1 = __byte_perm(e4m3x2_to_f16x2(sb), 0, ln.sel);
         const __half2 v0 = *reinterpret_cast<const __half2 *>(&h0), v1 = *reinterpret_cast<const __half2 *>(&h1);
-        if (Next) {
-            wait(r, r.full + 8u * c.slot, c.phase);
-            sl = slot();
-            s0 = lds16(sl + ln.scale);
-            s1 = lds16(sl + ln.scale + 32u);
-        }
+        if (next) wait_warp(r, bar, phase);
+        // (without a next window the loads read the slot all the same, and nobody uses them)
+        s0 = lds16(slot + ln.scale);
+        s1 = lds16(slot + ln.scale + 32u);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t a[4], b[4];
             e2m1x8_to_f16x2x4(w0[i], a);
             e2m1x8_to_f16x2x4(w1[i], b);
-            if (Next) {
-                w0[i] = lds32(sl + ln.code[i]);
-                w1[i] = lds32(sl + ln.code[i] + 128u);
-            }
-            const __half2 sa = i < 2 ? __low2half2(v0) : __high2half2(v0), sb = i < 2 ? __low2half2(v1) : __high2half2(v1);
+            w0[i] = lds32(slot + ln.code[i]);
+            w1[i] = lds32(slot + ln.code[i] + 128u);
+            const __half2 ma = i < 2 ? __low2half2(v0) : __high2half2(v0), mb = i < 2 ? __low2half2(v1) : __high2half2(v1);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                a[j] = mul_f16x2(a[j], sa);
-                b[j] = mul_f16x2(b[j], sb);
+                a[j] = mul_f16x2(a[j], ma);
+                b[j] = mul_f16x2(b[j], mb);
             }
 #pragma unroll
             for (int n = 0; n < N; ++n) {
@@ -273,7 +297,7 @@ struct Consumer {
                 mma_f16(acc.c[1][n], a[2], b[2], a[3], b[3], xv.z, xv.w);
             }
         }
-        if (Next) release();
+        if (next) release();
     }
     // One piece, the column tiles [ka, kb) of a row tile, whose first window is held; `more`: another
     // piece follows, whose first window is held afterwards. xa: the lane's token rows; `two`: the
@@ -283,29 +307,33 @@ struct Consumer {
         int w = ka & ~(kWindow - 1);
 #pragma unroll
         for (int n = 0; n < NT; ++n) x[n] = xa[n] + ln.x + (uint32_t)w * 128u;
-        for (; w < kb; w += kWindow) {
+        auto step = [&]() {
+            w += kWindow;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) x[n] += kWindow * 128u;
+        };
+        // a window of which the piece has only some units: a lane without a unit multiplies zeros by zero scales
+        // (zero times what an earlier window or an infinite activation left there could be a NaN)
+        auto part = [&]() {
+            const bool live = w + ln.unit >= ka && w + ln.unit < kb;
             uint32_t xl[NT];
-            uint32_t sa = s0, sb = s1;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) xl[n] = x[n];
-            if (w < ka || w + kWindow > kb) {
-                // only some of the window's units: a lane without a unit multiplies zeros by zero scales (zero times
-                // what an earlier window or an infinite activation left there could be a NaN)
-                if (w + ln.unit < ka || w + ln.unit >= kb) {
-                    sa = sb = 0u;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) xl[n] = r.zeros;
-                }
-            }
-            if (more || w + kWindow < kb) {
-                if (NT == 1 || !two) multiply<1, true>(xl, sa, sb, acc);
-                else multiply<NT, true>(xl, sa, sb, acc);
-            } else {
-                multiply<NT, false>(xl, sa, sb, acc);
-            }
+            for (int n = 0; n < NT; ++n) xl[n] = live ? x[n] : r.zeros;
+            multiply<NT>(xl, live ? s0 : 0u, live ? s1 : 0u, more || w + kWindow < kb, acc);
+            step();
+        };
+        if (w < ka) part();
+        const int whole = (kb - w) / kWindow;
+        const bool after = more || w + whole * kWindow < kb;
+#pragma unroll 1
+        for (int i = whole; i > 0; --i) {
+            if (NT == 1 || two) multiply<NT>(x, s0, s1, i > 1 || after, acc);
+            else multiply<1>(x, s0, s1, i > 1 || after, acc);
 #pragma unroll
             for (int n = 0; n < NT; ++n) x[n] += kWindow * 128u;
         }
+        w += whole * kWindow;
+        if (w < kb) part();
     }
 };
 
@@ -336,8 +364,9 @@ struct Pieces {
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumerThreads) : "memory"); }
 
 // The sums of a finished piece: warps 8 to 15 hand theirs to warps 0 to 7 through `buf` ([column][128
-// rows], kSumStride floats a column), and those call f(column, row of the tile, sum) for their values of
-// the first m columns, every lane of a warp in each call. The two warps of a row group meet at a barrier of
+// rows], kSumStride floats a column), and those call f(n, j, sum) for their values, every lane of a warp
+// in each call: column 8 n + 2 t + (j & 1) of m (beyond m where only other lanes have one), row
+// 16 warp + g + 8 (j >> 1). The two warps of a row group meet at a barrier of
 // their own; two buffers in turn make it one meeting per piece.
 constexpr int kSumStride = 132;
 template <int NT, class F>
@@ -360,7 +389,7 @@ __device__ __forceinline__ void join_pairs(const Acc<NT> &acc, float *buf, int m
                 if (8 * n + (j & 1) >= m) continue;          // no lane has a column below m
                 const int col = 8 * n + 2 * t + (j & 1);
                 const float other = col < m ? mine[(8 * n + (j & 1)) * kSumStride + 8 * (j >> 1)] : 0.f;
-                f(col, (warp & 7) * 16 + g + 8 * (j >> 1), acc.sum(n, j) + other);
+                f(n, j, acc.sum(n, j) + other);
             }
     }
 }
