@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
 
     router_logits(a, part);
     grid_arrive(arrive0);
-    convert_rows<8>(a.x, a.H, rows, a.T, a.H, KT1, emax, [](int) { return true; });
+    convert_rows<8, false>(a.x, a.H, rows, a.T, a.H, KT1, emax, [](int) { return true; });
     grid_wait(ring, arrive0, G);
     // counter 2 still holds the last call's arrivals; everyone's next use of it is behind barrier 1
     if (c == 0 && threadIdx.x == 0) *arrive2 = 0;

@@ -1,5 +1,6 @@
 // linear.cu -- the C ABI of the NVFP4 matrix product (tfmoe_linear_* in tfmoe.h): argument
 // checks, weight storage and repacking, and the choice of the regime.
+#include <algorithm>
 #include <cstdlib>
 #include <new>
 
@@ -15,7 +16,8 @@ namespace tfmoe {
 namespace {
 
 // One thread per (tiled row, column tile) copies 32 code bytes and 4 scale bytes into the
-// 128 x 64 tile layout of repack.cu; rows and columns past the matrix are zero. The source
+// 128 x 64 tile layout of repack.cu, except that the eight codes of a word are kept in the order
+// 0 2 4 6 1 3 5 7 (linear_tc.cu says why); rows and columns past the matrix are zero. The source
 // may start anywhere and its rows are K/2 and K/16 bytes long, so it is read byte by byte.
 __global__ void __launch_bounds__(256) linear_repack_kernel(
     const uint8_t *__restrict__ codes0, const uint8_t *__restrict__ scales0, const uint8_t *__restrict__ codes1,
@@ -33,60 +35,16 @@ __global__ void __launch_bounds__(256) linear_repack_kernel(
         const size_t tile = (size_t)(r / kTileRows) * KT + kt;
         uint8_t *ct = out_codes + tile * kTileCodeBytes + (r % kTileRows) * 16;
         uint8_t *st = out_scales + tile * kTileScaleBytes + (r % kTileRows) * 4;
-        for (int b = 0; b < 32; ++b) ct[(b >> 4) * 2048 + (b & 15)] = b < nc ? c[b] : 0;
+        for (int w = 0; w < 8; ++w) {
+            uint32_t lo = 0, hi = 0;                     // codes 0 2 4 6 and 1 3 5 7
+            for (int b = 0; b < 4; ++b) {
+                const uint32_t v = 4 * w + b < nc ? c[4 * w + b] : 0u;
+                lo |= (v & 15u) << (4 * b);
+                hi |= (v >> 4) << (4 * b);
+            }
+            *reinterpret_cast<uint32_t *>(ct + (w >> 2) * 2048 + (w & 3) * 4) = lo | hi << 16;
+        }
         for (int b = 0; b < 4; ++b) st[b] = b < ns ? sc[b] : 0;
-    }
-}
-
-// Simple form: one warp per output, lanes across the reduction, up to 4 tokens a pass.
-constexpr int kSimpleTokens = 4;
-__global__ void __launch_bounds__(256) linear_simple_kernel(const uint8_t *__restrict__ codes,
-                                                            const uint8_t *__restrict__ scales,
-                                                            const uint16_t *__restrict__ x, int64_t ldx, int T, int K,
-                                                            int KT, const LinearEpilogue ep)
-{
-    const int n = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (n >= ep.N) return;
-    const bool gated = ep.act == TFMOE_ACT_SWIGLU;
-    const float g0 = __ldg(ep.global0), g1 = gated ? __ldg(ep.global1) : 0.f;
-    for (int t0 = blockIdx.y * kSimpleTokens; t0 < T; t0 += gridDim.y * kSimpleTokens) {
-        float acc[2][kSimpleTokens] = {};
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            if (m == 1 && !gated) break;
-            const int r = gated ? 2 * n + m : n;
-            for (int k = lane * 8; k < K; k += 256) {
-                const size_t tile = (size_t)(r / kTileRows) * KT + k / kTileK;
-                const uint32_t w = *reinterpret_cast<const uint32_t *>(
-                    codes + tile * kTileCodeBytes + ((k >> 5) & 1) * 2048 + (r % kTileRows) * 16 + ((k & 31) >> 1));
-                const uint32_t sb = scales[tile * kTileScaleBytes + (r % kTileRows) * 4 + ((k & 63) >> 4)];
-                const float s = f16x2_to_float2(e4m3x2_to_f16x2(sb)).x;
-                uint32_t h[4];
-                e2m1x8_to_f16x2x4(w, h);
-#pragma unroll
-                for (int t = 0; t < kSimpleTokens; ++t) {
-                    if (t0 + t >= T) break;
-                    const uint4 xv = *reinterpret_cast<const uint4 *>(x + (int64_t)(t0 + t) * ldx + k);
-                    const uint32_t xu[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 wv = f16x2_to_float2(h[i]);
-                        acc[m][t] = fmaf(wv.x * s, bf16_bits_to_float(xu[i] & 0xFFFFu), acc[m][t]);
-                        acc[m][t] = fmaf(wv.y * s, bf16_bits_to_float(xu[i] >> 16), acc[m][t]);
-                    }
-                }
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < kSimpleTokens; ++t) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                acc[0][t] += __shfl_xor_sync(0xffffffffu, acc[0][t], o);
-                acc[1][t] += __shfl_xor_sync(0xffffffffu, acc[1][t], o);
-            }
-            if (lane == 0 && t0 + t < T)
-                store_output(ep, t0 + t, n, finish_output(ep, t0 + t, n, acc[0][t], acc[1][t], g0, g1));
-        }
     }
 }
 
@@ -98,16 +56,6 @@ cudaError_t launch_linear_repack(const Linear &L, const tfmoe_linear_weights &w,
     linear_repack_kernel<<<4 * L.num_sms, 256, 0, s>>>(w.codes, w.scales, gated ? w.up_codes : nullptr,
                                                        gated ? w.up_scales : nullptr, L.rows, L.desc.in_features,
                                                        L.RT, L.KT, L.codes, L.scales);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_linear_simple(Linear &L, const uint16_t *x, int64_t ldx, int T, const LinearEpilogue &ep,
-                                 cudaStream_t s, int *launches)
-{
-    const int chunks = (T + kSimpleTokens - 1) / kSimpleTokens;
-    dim3 grid((ep.N + 7) / 8, chunks < 1024 ? chunks : 1024);
-    linear_simple_kernel<<<grid, 256, 0, s>>>(L.codes, L.scales, x, ldx, T, L.desc.in_features, L.KT, ep);
-    *launches += 1;
     return cudaGetLastError();
 }
 
@@ -188,10 +136,12 @@ tfmoe_status tfmoe_linear_create(const tfmoe_linear_desc *desc, tfmoe_linear **o
     const size_t tiles = (size_t)L.RT * L.KT;
     const size_t small = 256 + (((size_t)L.rows * 4 + 255) & ~(size_t)255);      // global, bias
     e = cudaMalloc(&L.w_block, tiles * (kTileCodeBytes + kTileScaleBytes) + small);
-    L.zero_bytes = (256 + (size_t)L.RT * 4 + 255) & ~(size_t)255;
-    if (e == cudaSuccess) e = cudaMalloc(&L.ws_block, L.zero_bytes + linear_stream_partial_floats(L) * 4);
+    L.zero_bytes = (256 + (size_t)std::max(L.RT, L.num_sms) * 4 + 255) & ~(size_t)255;
+    const size_t sums = std::max(linear_stream_partial_floats(L), linear_tc_partial_floats(L));
+    if (e == cudaSuccess) e = cudaMalloc(&L.ws_block, L.zero_bytes + sums * 4);
     if (e == cudaSuccess) e = cudaMemset(L.ws_block, 0, L.zero_bytes);
     if (e == cudaSuccess) e = linear_stream_setup(L);
+    if (e == cudaSuccess) e = linear_tc_setup(L);
     if (e != cudaSuccess) {
         cudaGetLastError();
         if (L.w_block) cudaFree(L.w_block);
@@ -293,7 +243,7 @@ tfmoe_status tfmoe_linear_forward(tfmoe_linear *lin, const uint16_t *x, int64_t 
     const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
     const cudaError_t e = linear_stream_fits(L, T) && !(L.desc.flags & TFMOE_FLAG_FORCE_MMA)
                               ? launch_linear_stream(L, x, ldx, T, ep, s, &n)
-                              : launch_linear_simple(L, x, ldx, T, ep, s, &n);
+                              : launch_linear_tc(L, x, ldx, T, ep, s, &n);
     L.last_launches = n;
     if (e != cudaSuccess) return cuda_fail(e, who);
     return record_ok();

@@ -29,12 +29,12 @@ struct Linear {
     int RT = 0, KT = 0;               // row tiles of 128, column tiles of 64 (zero filled)
     void *w_block = nullptr;
     void *ws_block = nullptr;
-    uint8_t *codes = nullptr;         // [RT][KT] tiles of kTileCodeBytes
+    uint8_t *codes = nullptr;         // [RT][KT] tiles of kTileCodeBytes, words in the order 0 2 4 6 1 3 5 7
     uint8_t *scales = nullptr;        // [RT][KT] slabs of kTileScaleBytes
     float *global = nullptr;          // [2]
     float *bias = nullptr;            // [rows]
     int32_t *err_word = nullptr;
-    int32_t *tickets = nullptr;       // [RT] arrivals per row tile, 0 between calls
+    int32_t *tickets = nullptr;       // arrivals per row tile (streaming) or split tile, 0 between calls
     size_t zero_bytes = 0;            // err_word and tickets, at the start of the workspace
     float *partial = nullptr;         // sums of cut row tiles
     int32_t last_launches = 0;
@@ -43,13 +43,15 @@ struct Linear {
 inline bool linear_gated(const Linear &L) { return L.desc.activation == TFMOE_ACT_SWIGLU; }
 
 cudaError_t launch_linear_repack(const Linear &L, const tfmoe_linear_weights &w, cudaStream_t s);
-cudaError_t launch_linear_simple(Linear &L, const uint16_t *x, int64_t ldx, int T, const LinearEpilogue &ep,
-                                 cudaStream_t s, int *launches);
 bool linear_stream_fits(const Linear &L, int T);
 cudaError_t linear_stream_setup(const Linear &L);
 size_t linear_stream_partial_floats(const Linear &L);
 cudaError_t launch_linear_stream(Linear &L, const uint16_t *x, int64_t ldx, int T, const LinearEpilogue &ep,
                                  cudaStream_t s, int *launches);
+cudaError_t linear_tc_setup(const Linear &L);
+size_t linear_tc_partial_floats(const Linear &L);
+cudaError_t launch_linear_tc(Linear &L, const uint16_t *x, int64_t ldx, int T, const LinearEpilogue &ep,
+                             cudaStream_t s, int *launches);
 
 // Activations in fp32. expf, erff and the division are CUDA's own fp32 functions (a few units
 // in the last place), so an fp32 output keeps its precision.

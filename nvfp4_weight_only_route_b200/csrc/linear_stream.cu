@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
     grid_dep_wait();                                        // before anything another kernel may write
     {
         const bool all = q1 > q0 + 1;
-        convert_rows<8 * NT>(a.x, a.ldx, smem + lay.x, a.T, a.K, a.KT, emax, [&](int kg) {
+        convert_rows<8 * NT, true>(a.x, a.ldx, smem + lay.x, a.T, a.K, a.KT, emax, [&](int kg) {
             const bool from = kg >= k0 / 2, to = kg <= (k1 - 1) / 2;
             return all || (q1 == q0 ? from && to : from || to);
         }, requested);

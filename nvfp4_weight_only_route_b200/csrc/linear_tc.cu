@@ -1,0 +1,465 @@
+// linear_tc.cu -- the tensor-core regime of the NVFP4 matrix product: more tokens than the streaming
+// regime takes, bound by the bf16 tensor pipe (large T) or by latency (short prompts).
+//
+// A tile is 128 weight rows (MMA M) x N <= 192 tokens (MMA N), the reduction in stages of 64. The weights are
+// decoded to bf16 in registers and stored into tensor memory as the A operand; the bf16 token rows
+// come by TMA (128-byte swizzle) into shared memory as the B operand: no rounding of either. Per CTA
+// (one per SM, 24 warps):
+//   warp 0       token tiles (TMA) into a ring that the MMA commits free
+//   warp 2       codes and scales (bulk copies) into a ring that the decoders free
+//   warp 1       owns tensor memory, issues four MMAs of K = 16 per stage
+//   warps 4-15   three decode warpgroups taking every third stage, a thread per weight row
+//   warps 16-23  epilogue, two warpgroups taking alternate 16-token steps of the accumulator
+// Tensor memory: two accumulators of 192 columns, so that a tile's epilogue runs under the next tile's
+// products, and four decoded stages of 32 columns: all 512.
+//
+// The decode: a stage must be decoded in the time of its MMAs (2 N clocks, 384 at N = 192). A conversion
+// to f16 and on to bf16 would take about 410 clocks per stage of an SM's conversion rate (36 lanes per clock
+// for E2M1, 63 for f16 -> f32). So the code's bits are placed instead: sign at bit 15 and the three
+// magnitude bits at 8..6 of a bf16 are that E2M1 value times 2^-126, its subnormal included; one
+// bf16x2 multiplication by the block scale times 2^112 gives value * scale * 2^-14 exactly (at most 6
+// significant bits, 2^-24 to 0.17), and 2^14 joins the multiplier in the epilogue. The tiled layout
+// keeps the eight codes of a word in the order 0 2 4 6 1 3 5 7, so that a shift brings the codes of
+// columns 2j and 2j + 1 to the same place of both halves.
+//
+// Few tiles leave SMs idle, so their reductions are split: CTA (tile, split) leaves its sums in global memory,
+// and the CTA that arrives last at the tile's counter adds them in split order and finishes the tile.
+// No CTA waits for another; equal calls give equal bits.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "linear.h"
+
+namespace tfmoe {
+namespace {
+
+constexpr int kM = 128;
+constexpr int kMaxN = 192;
+constexpr int kBStages = 6, kAStages = 4, kCStages = 12, kDBufs = 2;
+constexpr int kDqGroups = 3, kEpiGroups = 2;
+constexpr int kDqWarp0 = 4, kEpiWarp0 = kDqWarp0 + 4 * kDqGroups;
+constexpr int kThreads = 32 * (kEpiWarp0 + 4 * kEpiGroups);
+constexpr int kEpiThreads = 128 * kEpiGroups;
+constexpr uint32_t kACol = kDBufs * kMaxN, kTmemCols = 512;
+static_assert(kACol + kAStages * 32 <= kTmemCols, "tensor memory");
+constexpr int kBBytes = kMaxN * 128;
+constexpr int kMaxSplits = 8;
+
+struct TcSmem {
+    uint8_t b[kBStages][kBBytes];            // 1024-byte aligned
+    uint8_t codes[kCStages][kTileCodeBytes];
+    uint8_t scales[kCStages][kTileScaleBytes];
+    uint64_t bfull[kBStages], bempty[kBStages];
+    uint64_t afull[kAStages], aempty[kAStages];
+    uint64_t cfull[kCStages], cempty[kCStages];
+    uint64_t dfull[kDBufs], dempty[kDBufs];
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    int32_t abort_flag;
+    int32_t is_last;
+};
+
+struct TcArgs {
+    const uint8_t *codes, *scales;
+    int T, RT, KT, N, splits, items;         // items: tiles * splits
+    float *partial;                          // [items][N][128]
+    int32_t *tickets;                        // [tiles], left at 0
+    int32_t *err_word;
+    LinearEpilogue ep;
+};
+
+__device__ __forceinline__ bool wait_or_abort(TcSmem &sm, uint64_t *bar, uint32_t parity, int32_t *err) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        for (int i = 0; i < 4; ++i)
+            if (mbar_try_wait_sleep(bar, parity)) return true;
+        if (*reinterpret_cast<volatile int32_t *>(&sm.abort_flag)) return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(err, DEV_ERR_WAIT_TIMEOUT);
+            *reinterpret_cast<volatile int32_t *>(&sm.abort_flag) = 1;
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool wait_warp(TcSmem &sm, uint64_t *bar, uint32_t parity, int32_t *err) {
+    return __all_sync(0xffffffffu, wait_or_abort(sm, bar, parity, err));
+}
+
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr) {
+    // K-major, 128-byte swizzle, 1024 bytes between groups of 8 rows
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1u << 16) | ((uint64_t)(1024u >> 4) << 32) |
+           ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+// kind::f16, A and B bf16 K-major, D fp32, M = 128.
+__device__ __forceinline__ uint32_t instr_desc(int n) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n\t}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(0u));
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t pred = 0;
+    asm volatile("{\n\t.reg .b32 rx;\n\t.reg .pred px;\n\telect.sync rx|px, %1;\n\t@px mov.s32 %0, 1;\n\t}"
+                 : "+r"(pred) : "r"(0xffffffffu));
+    return pred != 0;
+}
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
+
+// The block scales of two E4M3 bytes times 2^112, each in both halves of a bf16x2.
+__device__ __forceinline__ void scale_pairs(uint32_t two, uint32_t &lo, uint32_t &hi) {
+    const float2 f = f16x2_to_float2(e4m3x2_to_f16x2(two));
+    const uint32_t a = __float_as_uint(f.x * 0x1p112f), b = __float_as_uint(f.y * 0x1p112f);
+    lo = __byte_perm(a, 0, 0x3232);              // an E4M3 value fills 4 significant bits: its fp32 is a bf16
+    hi = __byte_perm(b, 0, 0x3232);
+}
+// Eight codes (order 0 2 4 6 1 3 5 7) times the scale pair -> four bf16x2, columns in order.
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t scale, uint32_t *o) {
+    constexpr uint32_t kSign = 0x80008000u, kMag = 0x01C001C0u;
+    const uint32_t v[4] = {((w << 12) & kSign) | ((w << 6) & kMag), ((w << 8) & kSign) | ((w << 2) & kMag),
+                           ((w << 4) & kSign) | ((w >> 2) & kMag), (w & kSign) | ((w >> 6) & kMag)};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[j]) : "r"(v[j]), "r"(scale));
+}
+
+struct Item {
+    int tile, split, rt, t0, k0, k1;
+    __device__ __forceinline__ Item(const TcArgs &a, int i) {
+        tile = i / a.splits;
+        split = i - tile * a.splits;
+        const int tt = tile / a.RT;              // row tiles first: concurrent tiles share token rows
+        rt = tile - tt * a.RT;
+        t0 = tt * a.N;
+        k0 = split * a.KT / a.splits;
+        k1 = (split + 1) * a.KT / a.splits;
+    }
+};
+
+// 16 tokens of a tile, t..t+15, of this lane's weight row: v(i) is token i's sum.
+template <class V>
+__device__ __forceinline__ void finish16(const TcArgs &a, int rt, int q, int t, float g0, float g1, V v) {
+    const LinearEpilogue &ep = a.ep;
+    const int row = rt * kM + q;
+    if (ep.act == TFMOE_ACT_SWIGLU) {
+        // an even lane has gate row j of the 16 tokens, the odd lane after it up row j: the even lane finishes
+        // tokens 0..7, the odd one 8..15
+        const bool odd = q & 1;
+        const int n = row >> 1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float lo = v(i), hi = v(i + 8);
+            const float keep = odd ? hi : lo, got = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+            const int tok = t + i + (odd ? 8 : 0);
+            if (tok < a.T && n < ep.N)
+                store_output(ep, tok, n, finish_output(ep, tok, n, odd ? got : keep, odd ? keep : got, g0, g1));
+        }
+    } else if (row < ep.N) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (t + i < a.T) store_output(ep, t + i, row, finish_output(ep, t + i, row, v(i), 0.f, g0, 0.f));
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_constant__ CUtensorMap xmap, const TcArgs a)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    TcSmem &sm = *reinterpret_cast<TcSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kBStages; ++s) { mbar_init(&sm.bfull[s], 1); mbar_init(&sm.bempty[s], 1); }
+        for (int s = 0; s < kAStages; ++s) { mbar_init(&sm.afull[s], 4); mbar_init(&sm.aempty[s], 1); }
+        for (int s = 0; s < kCStages; ++s) { mbar_init(&sm.cfull[s], 1); mbar_init(&sm.cempty[s], 4); }
+        for (int s = 0; s < kDBufs; ++s) { mbar_init(&sm.dfull[s], 1); mbar_init(&sm.dempty[s], 4 * kEpiGroups); }
+        mbar_init(&sm.mma_done, 1);
+        sm.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(&sm.tmem_base)), "r"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    grid_dep_launch_dependents();
+    const uint32_t tmem = sm.tmem_base;
+    int32_t *err = a.err_word;
+
+    if (warp == 0 || warp == 2) {
+        if (lane == 0) {
+            const bool tokens = warp == 0;
+            const int nst = tokens ? kBStages : kCStages;
+            uint64_t *full = tokens ? sm.bfull : sm.cfull, *empty = tokens ? sm.bempty : sm.cempty;
+            if (tokens) grid_dep_wait();         // the weights are nobody's output; the tokens may be
+            uint32_t issued = 0, ph = 0;
+            int s = 0;
+            bool ok = true;
+            for (int i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
+                const Item it(a, i);
+                for (int kt = it.k0; kt < it.k1; ++kt) {
+                    ok = wait_or_abort(sm, &empty[s], ph ^ 1u, err);
+                    if (!ok) break;
+                    if (tokens) {
+                        mbar_arrive_expect_tx(&full[s], (uint32_t)a.N * 128u);
+                        tma_load_2d(sm.b[s], &xmap, kt * kTileK, it.t0, &full[s]);
+                    } else {
+                        const size_t tile = (size_t)it.rt * a.KT + kt;
+                        mbar_arrive_expect_tx(&full[s], kTileCodeBytes + kTileScaleBytes);
+                        bulk_g2s(sm.codes[s], a.codes + tile * kTileCodeBytes, kTileCodeBytes, &full[s]);
+                        bulk_g2s(sm.scales[s], a.scales + tile * kTileScaleBytes, kTileScaleBytes, &full[s]);
+                    }
+                    ++issued;
+                    if (++s == nst) { s = 0; ph ^= 1u; }
+                }
+            }
+            if (*reinterpret_cast<volatile int32_t *>(&sm.abort_flag)) {
+                // aborted: let the copies already issued land before the CTA exits (bounded)
+                for (uint32_t j = issued > (uint32_t)nst ? issued - nst : 0; j < issued; ++j) {
+                    const uint64_t t0 = global_timer_ns();
+                    while (!mbar_try_wait_sleep(&full[j % nst], (j / nst) & 1u) && global_timer_ns() - t0 < kWaitLimitNs / 4) {
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        const uint64_t bdesc0 = smem_desc(smem_u32(sm.b[0]));
+        int sa = 0, sb = 0;
+        uint32_t pa = 0, pb = 0, n_item = 0;
+        bool ok = true;
+        for (int i = blockIdx.x; i < a.items && ok; i += gridDim.x, ++n_item) {
+            const Item it(a, i);
+            const uint32_t idesc = instr_desc(min(a.N, (a.T - it.t0 + 15) & ~15));
+            const int buf = (int)(n_item % kDBufs);
+            ok = wait_warp(sm, &sm.dempty[buf], ((n_item / kDBufs) & 1u) ^ 1u, err);
+            if (!ok) break;
+            tc_after();
+            const uint32_t d = tmem + (uint32_t)buf * kMaxN;
+            for (int kt = it.k0; kt < it.k1; ++kt) {
+                ok = wait_warp(sm, &sm.bfull[sb], pb, err) && wait_warp(sm, &sm.afull[sa], pa, err);
+                if (!ok) break;
+                tc_after();
+                if (elect_one()) {
+                    const uint64_t bd = bdesc0 + (uint64_t)(sb * (kBBytes >> 4));
+                    const uint32_t ad = tmem + kACol + (uint32_t)sa * 32u;
+                    mma_ts(d, ad, bd, idesc, kt != it.k0);
+                    mma_ts(d, ad + 8u, bd + 2u, idesc, 1u);
+                    mma_ts(d, ad + 16u, bd + 4u, idesc, 1u);
+                    mma_ts(d, ad + 24u, bd + 6u, idesc, 1u);
+                    commit(&sm.bempty[sb]);
+                    commit(&sm.aempty[sa]);
+                }
+                __syncwarp();
+                if (++sa == kAStages) { sa = 0; pa ^= 1u; }
+                if (++sb == kBStages) { sb = 0; pb ^= 1u; }
+            }
+            if (!ok) break;
+            if (elect_one()) commit(&sm.dfull[buf]);
+            __syncwarp();
+        }
+        // on every path: tensor memory and the stages stay in use until the MMAs issued are complete
+        if (elect_one()) commit(&sm.mma_done);
+        __syncwarp();
+    } else if (warp >= kDqWarp0 && warp < kEpiWarp0) {
+        const int gq = (warp - kDqWarp0) >> 2, q = (warp & 3) * 32 + lane;
+        const uint32_t acol = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kACol;
+        uint32_t g = 0;                          // running stage number
+        bool ok = true;
+        for (int i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
+            const Item it(a, i);
+            for (int kt = it.k0; kt < it.k1; ++kt, ++g) {
+                if ((int)(g % kDqGroups) != gq) continue;
+                const uint32_t sc = g % kCStages, sa = g % kAStages;
+                ok = wait_warp(sm, &sm.cfull[sc], (g / kCStages) & 1u, err);
+                if (!ok) break;
+                const uint4 c0 = *reinterpret_cast<const uint4 *>(sm.codes[sc] + q * 16);
+                const uint4 c1 = *reinterpret_cast<const uint4 *>(sm.codes[sc] + 2048 + q * 16);
+                const uint32_t sc4 = *reinterpret_cast<const uint32_t *>(sm.scales[sc] + q * 4);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.cempty[sc]);
+                uint32_t s[4], r[32];
+                scale_pairs(sc4 & 0xFFFFu, s[0], s[1]);
+                scale_pairs(sc4 >> 16, s[2], s[3]);
+                const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+                for (int w = 0; w < 8; ++w) decode8(words[w], s[w >> 1], r + 4 * w);
+                ok = wait_warp(sm, &sm.aempty[sa], ((g / kAStages) & 1u) ^ 1u, err);
+                if (!ok) break;
+                tc_after();
+                tmem_st16(acol + sa * 32u, r);
+                tmem_st16(acol + sa * 32u + 16u, r + 16);
+                tc_wait_st();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.afull[sa]);
+            }
+        }
+    } else if (warp >= kEpiWarp0) {
+        const int eg = (warp - kEpiWarp0) >> 2, q = (warp & 3) * 32 + lane;
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const float g0 = __ldg(a.ep.global0) * 0x1p14f, g1 = a.ep.act == TFMOE_ACT_SWIGLU ? __ldg(a.ep.global1) * 0x1p14f : 0.f;
+        grid_dep_wait();
+        uint32_t n_item = 0;
+        for (int i = blockIdx.x; i < a.items; i += gridDim.x, ++n_item) {
+            const Item it(a, i);
+            const int buf = (int)(n_item % kDBufs);
+            const int steps = (min(a.N, a.T - it.t0) + 15) >> 4;
+            // after an abort a split item's warps still meet at the barriers below, and read nothing
+            const bool ok = wait_warp(sm, &sm.dfull[buf], (n_item / kDBufs) & 1u, err);
+            if (!ok && a.splits == 1) break;
+            tc_after();
+            const uint32_t d = tmem + lane_base + (uint32_t)buf * kMaxN;
+            float *mine = a.partial + (size_t)i * a.N * kM + q;
+            for (int st = ok ? eg : steps; st < steps; st += kEpiGroups) {
+                uint32_t r[16];
+                tmem_ld16(d + (uint32_t)(st * 16), r);
+                tc_wait_ld();
+                if (st + kEpiGroups >= steps) {  // the warp's last read of the accumulator
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.dempty[buf]);
+                }
+                if (a.splits == 1) {
+                    finish16(a, it.rt, q, it.t0 + st * 16, g0, g1, [&](int j) { return __uint_as_float(r[j]); });
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) mine[(size_t)(st * 16 + j) * kM] = __uint_as_float(r[j]);
+                }
+            }
+            if (ok && eg >= steps) {
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.dempty[buf]);
+            }
+            if (a.splits == 1) continue;
+            epilogue_sync();
+            if (threadIdx.x == kEpiWarp0 * 32) {
+                __threadfence();                 // the CTA's sums, ordered by the barrier
+                const int last = atomicAdd(a.tickets + it.tile, 1) == a.splits - 1;
+                if (last) a.tickets[it.tile] = 0;
+                __threadfence();
+                sm.is_last = last;
+            }
+            epilogue_sync();
+            if (sm.is_last) {
+                const float *src = a.partial + (size_t)it.tile * a.splits * a.N * kM + q;
+                const size_t stride = (size_t)a.N * kM;
+                for (int st = eg; st < steps; st += kEpiGroups) {
+                    float v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = __ldcg(src + (size_t)(st * 16 + j) * kM);
+                    for (int s = 1; s < a.splits; ++s) {
+                        float u[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) u[j] = __ldcg(src + s * stride + (size_t)(st * 16 + j) * kM);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] += u[j];
+                    }
+                    finish16(a, it.rt, q, it.t0 + st * 16, g0, g1, [&](int j) { return v[j]; });
+                }
+            }
+            epilogue_sync();                     // is_last is free again
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        if (lane == 0) mbar_wait_bounded(&sm.mma_done, 0, err);
+        __syncwarp();
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+    }
+}
+
+constexpr size_t kSmemBytes = sizeof(TcSmem) + 1024;
+
+struct TcPlan {
+    int N, splits;
+};
+
+// The tile width and the number of splits with the least estimated time, in clocks of an SM. A stage of 64
+// columns takes its MMAs' time, or the decode's where N is small; a wave ends with its last epilogue
+// (about 6 clocks an output of the 128 rows); splits add the sums' way to global memory and back.
+TcPlan make_tc_plan(const Linear &L, int T) {
+    TcPlan best{16, 1};
+    double least = 1e30;
+    for (int N = 16; N <= kMaxN; N += 16) {
+        const int64_t tiles = (int64_t)L.RT * ((T + N - 1) / N);
+        for (int S = 1; S <= kMaxSplits && S <= L.KT; ++S) {
+            if (S > 1 && tiles * S > L.num_sms) break;         // the workspace holds one wave of sums
+            const int64_t waves = (tiles * S + L.num_sms - 1) / L.num_sms;
+            const double stage = std::max(2.0 * N, 230.0), stages = (double)((L.KT + S - 1) / S);
+            double t = (double)waves * stages * stage + 6.0 * N + 3000.0;
+            if (S > 1) t += 3000.0 + 10.0 * N + 8.0 * N * S;
+            if (t < least) { least = t; best = {N, S}; }
+        }
+        if (N >= T) break;
+    }
+    return best;
+}
+
+}  // namespace
+
+cudaError_t linear_tc_setup(const Linear &)
+{
+    return cudaFuncSetAttribute(linear_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+}
+
+size_t linear_tc_partial_floats(const Linear &L) {
+    return (size_t)L.num_sms * std::min(kMaxN, (L.desc.max_tokens + 15) & ~15) * kM;
+}
+
+cudaError_t launch_linear_tc(Linear &L, const uint16_t *x, int64_t ldx, int T, const LinearEpilogue &ep, cudaStream_t s,
+                             int *launches)
+{
+    const TcPlan plan = make_tc_plan(L, T);
+    TcArgs a{};
+    a.codes = L.codes; a.scales = L.scales;
+    a.T = T; a.RT = L.RT; a.KT = L.KT;
+    a.N = plan.N; a.splits = plan.splits;
+    a.items = L.RT * ((T + plan.N - 1) / plan.N) * plan.splits;
+    a.partial = L.partial; a.tickets = L.tickets; a.err_word = L.err_word;
+    a.ep = ep;
+    CUtensorMap map;
+    if (encode_tensor_map_2d(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, const_cast<uint16_t *>(x), (uint64_t)L.desc.in_features,
+                             (uint64_t)T, (uint64_t)ldx * 2, (uint32_t)kTileK, (uint32_t)plan.N,
+                             CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(std::min(L.num_sms, a.items));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_tc_kernel, map, a);
+    *launches += 1;
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace tfmoe

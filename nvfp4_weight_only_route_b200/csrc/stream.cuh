@@ -394,13 +394,23 @@ __device__ __forceinline__ void join_pairs(const Acc<NT> &acc, float *buf, int m
     }
 }
 
-// Eight bf16 values (as loaded) times `up`, rounded to f16.
+// Eight bf16 values (as loaded) times `up`, rounded to f16; in the order 0 2 4 6 1 3 5 7 when the weights'
+// words are kept so (the matrix product's).
+template <bool EvenFirst>
 __device__ __forceinline__ uint4 bf16x8_to_f16(const uint4 &v, float up) {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    float lo[4], hi[4];
     uint32_t o[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const __half2 h = __floats2half2_rn(bf16_bits_to_float(u[j] & 0xFFFFu) * up, bf16_bits_to_float(u[j] >> 16) * up);
+        lo[j] = bf16_bits_to_float(u[j] & 0xFFFFu) * up;
+        hi[j] = bf16_bits_to_float(u[j] >> 16) * up;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __half2 h = !EvenFirst ? __floats2half2_rn(lo[j], hi[j])
+                          : j < 2    ? __floats2half2_rn(lo[2 * j], lo[2 * j + 1])
+                                     : __floats2half2_rn(hi[2 * j - 4], hi[2 * j - 3]);
         o[j] = *reinterpret_cast<const uint32_t *>(&h);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
@@ -430,7 +440,7 @@ __device__ __forceinline__ float inverse_up(uint32_t emax) {
 // keeps up to kHeld chunks in registers between finding the maximum and converting; what lies beyond
 // is read again. requested: an
 // mbarrier that every consumer warp arrives at once its first loads are on the way.
-template <int kHeld, class Used>
+template <int kHeld, bool EvenFirst, class Used>
 __device__ __forceinline__ void convert_rows(const uint16_t *x, int64_t ld, uint8_t *rows, int T, int K, int KT,
                                              uint32_t *emax, Used used, uint32_t requested = 0) {
     const int chunks = ((KT + 1) / 2) * 16;
@@ -468,13 +478,13 @@ __device__ __forceinline__ void convert_rows(const uint16_t *x, int64_t ld, uint
         for (int j = 0; j < kHeld; ++j) {
             const int i = i0 + j * tpr;
             if (j >= rounds) break;
-            if (i < chunks && used(i >> 4)) *reinterpret_cast<uint4 *>(dst + chunk_offset(i * 8)) = bf16x8_to_f16(v[j], up);
+            if (i < chunks && used(i >> 4)) *reinterpret_cast<uint4 *>(dst + chunk_offset(i * 8)) = bf16x8_to_f16<EvenFirst>(v[j], up);
         }
 #pragma unroll 4
         for (int i = i0 + kHeld * tpr; i < chunks; i += tpr)
             if (used(i >> 4))
                 *reinterpret_cast<uint4 *>(dst + chunk_offset(i * 8)) =
-                    i * 8 < K ? bf16x8_to_f16(row[i], up) : make_uint4(0, 0, 0, 0);
+                    i * 8 < K ? bf16x8_to_f16<EvenFirst>(row[i], up) : make_uint4(0, 0, 0, 0);
     }
     consumer_sync();
 }
