@@ -1,7 +1,7 @@
 // linear_tc.cu -- the tensor-core regime of the NVFP4 matrix product: more tokens than the streaming
 // regime takes, bound by the bf16 tensor pipe (large T) or by latency (short prompts).
 //
-// A tile is 128 weight rows (MMA M) x N <= 192 tokens (MMA N), the reduction in stages of 64. The weights are
+// A tile is 128 weight rows (MMA M) x N <= 224 tokens (MMA N), the reduction in stages of 64. The weights are
 // decoded to bf16 in registers and stored into tensor memory as the A operand; the bf16 token rows
 // come by TMA (128-byte swizzle) into shared memory as the B operand: no rounding of either. Per CTA
 // (one per SM, 24 warps):
@@ -10,10 +10,18 @@
 //   warp 1       owns tensor memory, issues four MMAs of K = 16 per stage
 //   warps 4-15   three decode warpgroups taking every third stage, a thread per weight row
 //   warps 16-23  epilogue, two warpgroups taking alternate 16-token steps of the accumulator
-// Tensor memory: two accumulators of 192 columns, so that a tile's epilogue runs under the next tile's
-// products, and four decoded stages of 32 columns: all 512.
+// Tensor memory: the accumulator at columns [0, 224), five decoded stages of 32 columns from 256.
 //
-// The decode: a stage must be decoded in the time of its MMAs (2 N clocks, 384 at N = 192). A conversion
+// What bounds the main loop is the issue: four MMAs, a commit and a barrier wait cost the issuing warp about
+// 460 clocks (two accumulators of 192 columns, 384 clocks of MMA per stage, ran at 680 with two waits
+// and two commits), so a stage's decoders wait for its token tile too, one barrier and one commit
+// serve both operands, the next stage's barrier is asked before the current MMAs are issued, and the
+// tile is as wide as the epilogue can take out of tensor memory at once: its 256 threads load the whole
+// accumulator into registers (up to 112 each), hand it back within a few hundred clocks, and finish
+// the tile under the next one's products. The register split follows from that: 144 for the epilogue,
+// 48 for the others.
+//
+// The decode: a stage must be decoded in the time of its MMAs (2 N clocks, 416 at N = 208). A conversion
 // to f16 and on to bf16 would take about 410 clocks per stage of an SM's conversion rate (36 lanes per clock
 // for E2M1, 63 for f16 -> f32). So the code's bits are placed instead: sign at bit 15 and the three
 // magnitude bits at 8..6 of a bf16 are that E2M1 value times 2^-126, its subnormal included; one
@@ -35,25 +43,29 @@ namespace tfmoe {
 namespace {
 
 constexpr int kM = 128;
-constexpr int kMaxN = 192;
-constexpr int kBStages = 6, kAStages = 4, kCStages = 12, kDBufs = 2;
+constexpr int kMaxN = 224;
+constexpr int kStages = 5, kCStages = 12;
 constexpr int kDqGroups = 3, kEpiGroups = 2;
 constexpr int kDqWarp0 = 4, kEpiWarp0 = kDqWarp0 + 4 * kDqGroups;
 constexpr int kThreads = 32 * (kEpiWarp0 + 4 * kEpiGroups);
 constexpr int kEpiThreads = 128 * kEpiGroups;
-constexpr uint32_t kACol = kDBufs * kMaxN, kTmemCols = 512;
-static_assert(kACol + kAStages * 32 <= kTmemCols, "tensor memory");
+constexpr int kHeld = kMaxN / 16 / kEpiGroups;       // 16-token steps an epilogue thread holds
+constexpr uint32_t kACol = 256, kTmemCols = 512;
+static_assert(kMaxN <= (int)kACol && kACol + kStages * 32 <= kTmemCols, "tensor memory");
+static_assert(kMaxN % (16 * kEpiGroups) == 0, "even share of the steps");
 constexpr int kBBytes = kMaxN * 128;
 constexpr int kMaxSplits = 8;
+// 768 threads start with 80 registers (61440 in all).
+constexpr int kEpiRegs = 144, kOtherRegs = 48;
+static_assert(kEpiThreads * kEpiRegs + (kThreads - kEpiThreads) * kOtherRegs <= kThreads * 80, "register split");
 
 struct TcSmem {
-    uint8_t b[kBStages][kBBytes];            // 1024-byte aligned
+    uint8_t b[kStages][kBBytes];             // 1024-byte aligned
     uint8_t codes[kCStages][kTileCodeBytes];
     uint8_t scales[kCStages][kTileScaleBytes];
-    uint64_t bfull[kBStages], bempty[kBStages];
-    uint64_t afull[kAStages], aempty[kAStages];
+    uint64_t bfull[kStages], ready[kStages], empty[kStages];
     uint64_t cfull[kCStages], cempty[kCStages];
-    uint64_t dfull[kDBufs], dempty[kDBufs];
+    uint64_t dfull, dempty;
     uint64_t mma_done;
     uint32_t tmem_base;
     int32_t abort_flag;
@@ -85,6 +97,14 @@ __device__ __forceinline__ bool wait_or_abort(TcSmem &sm, uint64_t *bar, uint32_
 }
 __device__ __forceinline__ bool wait_warp(TcSmem &sm, uint64_t *bar, uint32_t parity, int32_t *err) {
     return __all_sync(0xffffffffu, wait_or_abort(sm, bar, parity, err));
+}
+
+// Whether a phase is complete, without waiting.
+__device__ __forceinline__ bool test_now(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
 }
 
 __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr) {
@@ -158,41 +178,83 @@ struct Item {
     }
 };
 
-// 16 tokens of a tile, t..t+15, of this lane's weight row: v(i) is token i's sum.
-template <class V>
-__device__ __forceinline__ void finish16(const TcArgs &a, int rt, int q, int t, float g0, float g1, V v) {
-    const LinearEpilogue &ep = a.ep;
-    const int row = rt * kM + q;
-    if (ep.act == TFMOE_ACT_SWIGLU) {
-        // an even lane has gate row j of the 16 tokens, the odd lane after it up row j: the even lane finishes
-        // tokens 0..7, the odd one 8..15
-        const bool odd = q & 1;
-        const int n = row >> 1;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float lo = v(i), hi = v(i + 8);
-            const float keep = odd ? hi : lo, got = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
-            const int tok = t + i + (odd ? 8 : 0);
-            if (tok < a.T && n < ep.N)
-                store_output(ep, tok, n, finish_output(ep, tok, n, odd ? got : keep, odd ? keep : got, g0, g1));
-        }
-    } else if (row < ep.N) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (t + i < a.T) store_output(ep, t + i, row, finish_output(ep, t + i, row, v(i), 0.f, g0, 0.f));
+// The activation for outputs that are rounded to bf16: exponential and reciprocal one instruction each
+// (relative errors of a few units of fp32). fp32 outputs take CUDA's own functions (linear.h).
+__device__ __forceinline__ float activate_fast(float y, int act) {
+    switch (act) {
+    case TFMOE_ACT_SILU: return silu_f32(y);
+    case TFMOE_ACT_GELU_TANH: {
+        const float z = 1.5957691216057308f * (y + 0.044715f * y * y * y);
+        return y * rcp_approx(1.0f + __expf(-z));
+    }
+    default: return activate(y, act);
     }
 }
 
+// The held sums of one epilogue thread: step j is tokens t0 + 16 (2 j + eg) .. + 15 of this lane's weight row.
+template <int Act, bool Fast>
+__device__ __forceinline__ void finish_held(const TcArgs &a, int rt, int q, int t0, int eg, int steps, float g0, float g1,
+                                            const uint32_t (&r)[kHeld][16]) {
+    const LinearEpilogue &ep = a.ep;
+    auto act = [&](float y) { return Fast ? activate_fast(y, Act) : activate(y, Act); };
+    if (Act == TFMOE_ACT_SWIGLU) {
+        // an even lane has gate row j of the 16 tokens, the odd lane after it up row j: the even lane finishes
+        // tokens 0..7, the odd one 8..15
+        const bool odd = q & 1;
+        const int n = (rt * kM + q) >> 1;
+        const float b0 = ep.bias && n < ep.N ? __ldg(ep.bias + n) : 0.f, b1 = ep.bias && n < ep.N ? __ldg(ep.bias + ep.N + n) : 0.f;
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) {
+            if (2 * j + eg >= steps) continue;
+            const int t = t0 + 16 * (2 * j + eg) + (odd ? 8 : 0);
+            const uint16_t *res = ep.residual ? ep.residual + (int64_t)t * ep.ldr + n : nullptr;
+            char *out = static_cast<char *>(ep.out) + ((int64_t)t * ep.ldo + n) * (Fast ? 2 : 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float lo = __uint_as_float(r[j][i]), hi = __uint_as_float(r[j][i + 8]);
+                const float keep = odd ? hi : lo, got = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+                const float gate = fmaf(odd ? got : keep, g0, b0), up = fmaf(odd ? keep : got, g1, b1);
+                if (t + i < a.T && n < ep.N) {
+                    float v = (Fast ? silu_f32(gate) : activate(gate, TFMOE_ACT_SILU)) * up;
+                    if (res) v += bf16_bits_to_float(res[i * ep.ldr]);
+                    if (Fast) *reinterpret_cast<uint16_t *>(out + i * ep.ldo * 2) = float_to_bf16_bits_rn(v);
+                    else *reinterpret_cast<float *>(out + i * ep.ldo * 4) = v;
+                }
+            }
+        }
+    } else {
+        const int n = rt * kM + q;
+        if (n >= ep.N) return;
+        const float b0 = ep.bias ? __ldg(ep.bias + n) : 0.f;
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) {
+            if (2 * j + eg >= steps) continue;
+            const int t = t0 + 16 * (2 * j + eg);
+            const uint16_t *res = ep.residual ? ep.residual + (int64_t)t * ep.ldr + n : nullptr;
+            char *out = static_cast<char *>(ep.out) + ((int64_t)t * ep.ldo + n) * (Fast ? 2 : 4);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (t + i >= a.T) break;
+                float v = act(fmaf(__uint_as_float(r[j][i]), g0, b0));
+                if (res) v += bf16_bits_to_float(res[i * ep.ldr]);
+                if (Fast) *reinterpret_cast<uint16_t *>(out + i * ep.ldo * 2) = float_to_bf16_bits_rn(v);
+                else *reinterpret_cast<float *>(out + i * ep.ldo * 4) = v;
+            }
+        }
+    }
+}
+
+template <int Act, bool Fast>
 __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_constant__ CUtensorMap xmap, const TcArgs a)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     TcSmem &sm = *reinterpret_cast<TcSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kBStages; ++s) { mbar_init(&sm.bfull[s], 1); mbar_init(&sm.bempty[s], 1); }
-        for (int s = 0; s < kAStages; ++s) { mbar_init(&sm.afull[s], 4); mbar_init(&sm.aempty[s], 1); }
+        for (int s = 0; s < kStages; ++s) { mbar_init(&sm.bfull[s], 1); mbar_init(&sm.ready[s], 4); mbar_init(&sm.empty[s], 1); }
         for (int s = 0; s < kCStages; ++s) { mbar_init(&sm.cfull[s], 1); mbar_init(&sm.cempty[s], 4); }
-        for (int s = 0; s < kDBufs; ++s) { mbar_init(&sm.dfull[s], 1); mbar_init(&sm.dempty[s], 4 * kEpiGroups); }
+        mbar_init(&sm.dfull, 1);
+        mbar_init(&sm.dempty, 4 * kEpiGroups);
         mbar_init(&sm.mma_done, 1);
         sm.abort_flag = 0;
         fence_mbar_init();
@@ -209,11 +271,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     const uint32_t tmem = sm.tmem_base;
     int32_t *err = a.err_word;
 
-    if (warp == 0 || warp == 2) {
+    if (warp < kDqWarp0) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+      if (warp == 0 || warp == 2) {
         if (lane == 0) {
             const bool tokens = warp == 0;
-            const int nst = tokens ? kBStages : kCStages;
-            uint64_t *full = tokens ? sm.bfull : sm.cfull, *empty = tokens ? sm.bempty : sm.cempty;
+            const int nst = tokens ? kStages : kCStages;
+            uint64_t *full = tokens ? sm.bfull : sm.cfull, *empty = tokens ? sm.empty : sm.cempty;
             if (tokens) grid_dep_wait();         // the weights are nobody's output; the tokens may be
             uint32_t issued = 0, ph = 0;
             int s = 0;
@@ -245,143 +309,161 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 }
             }
         }
-    } else if (warp == 1) {
+      } else if (warp == 1) {
         const uint64_t bdesc0 = smem_desc(smem_u32(sm.b[0]));
-        int sa = 0, sb = 0;
-        uint32_t pa = 0, pb = 0, n_item = 0;
+        int s = 0;
+        uint32_t ph = 0, n_item = 0;
         bool ok = true;
         for (int i = blockIdx.x; i < a.items && ok; i += gridDim.x, ++n_item) {
             const Item it(a, i);
             const uint32_t idesc = instr_desc(min(a.N, (a.T - it.t0 + 15) & ~15));
-            const int buf = (int)(n_item % kDBufs);
-            ok = wait_warp(sm, &sm.dempty[buf], ((n_item / kDBufs) & 1u) ^ 1u, err);
+            ok = wait_warp(sm, &sm.dempty, (n_item & 1u) ^ 1u, err);
             if (!ok) break;
-            tc_after();
-            const uint32_t d = tmem + (uint32_t)buf * kMaxN;
+            bool here = test_now(&sm.ready[s], ph);
             for (int kt = it.k0; kt < it.k1; ++kt) {
-                ok = wait_warp(sm, &sm.bfull[sb], pb, err) && wait_warp(sm, &sm.afull[sa], pa, err);
-                if (!ok) break;
+                if (!__all_sync(0xffffffffu, here)) {
+                    ok = wait_warp(sm, &sm.ready[s], ph, err);
+                    if (!ok) break;
+                }
                 tc_after();
+                // the next stage's barrier is asked while this one's MMAs are issued
+                const int sn = s + 1 == kStages ? 0 : s + 1;
+                const uint32_t pn = ph ^ (sn == 0 ? 1u : 0u);
+                here = test_now(&sm.ready[sn], pn);
                 if (elect_one()) {
-                    const uint64_t bd = bdesc0 + (uint64_t)(sb * (kBBytes >> 4));
-                    const uint32_t ad = tmem + kACol + (uint32_t)sa * 32u;
-                    mma_ts(d, ad, bd, idesc, kt != it.k0);
-                    mma_ts(d, ad + 8u, bd + 2u, idesc, 1u);
-                    mma_ts(d, ad + 16u, bd + 4u, idesc, 1u);
-                    mma_ts(d, ad + 24u, bd + 6u, idesc, 1u);
-                    commit(&sm.bempty[sb]);
-                    commit(&sm.aempty[sa]);
+                    const uint64_t bd = bdesc0 + (uint64_t)(s * (kBBytes >> 4));
+                    const uint32_t ad = tmem + kACol + (uint32_t)s * 32u;
+                    mma_ts(tmem, ad, bd, idesc, kt != it.k0);
+                    mma_ts(tmem, ad + 8u, bd + 2u, idesc, 1u);
+                    mma_ts(tmem, ad + 16u, bd + 4u, idesc, 1u);
+                    mma_ts(tmem, ad + 24u, bd + 6u, idesc, 1u);
+                    commit(&sm.empty[s]);
                 }
                 __syncwarp();
-                if (++sa == kAStages) { sa = 0; pa ^= 1u; }
-                if (++sb == kBStages) { sb = 0; pb ^= 1u; }
+                s = sn;
+                ph = pn;
             }
             if (!ok) break;
-            if (elect_one()) commit(&sm.dfull[buf]);
+            if (elect_one()) commit(&sm.dfull);
             __syncwarp();
         }
         // on every path: tensor memory and the stages stay in use until the MMAs issued are complete
         if (elect_one()) commit(&sm.mma_done);
         __syncwarp();
-    } else if (warp >= kDqWarp0 && warp < kEpiWarp0) {
+      }
+    } else if (warp < kEpiWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         const int gq = (warp - kDqWarp0) >> 2, q = (warp & 3) * 32 + lane;
         const uint32_t acol = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kACol;
-        uint32_t g = 0;                          // running stage number
+        // this group's stages are the running numbers gq, gq + 3, ...
+        int skip = gq;
+        uint32_t sc = gq % kCStages, pc = 0, s = gq % kStages, ph = 0;
         bool ok = true;
         for (int i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
             const Item it(a, i);
-            for (int kt = it.k0; kt < it.k1; ++kt, ++g) {
-                if ((int)(g % kDqGroups) != gq) continue;
-                const uint32_t sc = g % kCStages, sa = g % kAStages;
-                ok = wait_warp(sm, &sm.cfull[sc], (g / kCStages) & 1u, err);
+            int kt = it.k0 + skip;
+            for (; kt < it.k1; kt += kDqGroups) {
+                ok = wait_warp(sm, &sm.cfull[sc], pc, err);
                 if (!ok) break;
                 const uint4 c0 = *reinterpret_cast<const uint4 *>(sm.codes[sc] + q * 16);
                 const uint4 c1 = *reinterpret_cast<const uint4 *>(sm.codes[sc] + 2048 + q * 16);
                 const uint32_t sc4 = *reinterpret_cast<const uint32_t *>(sm.scales[sc] + q * 4);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.cempty[sc]);
-                uint32_t s[4], r[32];
-                scale_pairs(sc4 & 0xFFFFu, s[0], s[1]);
-                scale_pairs(sc4 >> 16, s[2], s[3]);
-                const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-                for (int w = 0; w < 8; ++w) decode8(words[w], s[w >> 1], r + 4 * w);
-                ok = wait_warp(sm, &sm.aempty[sa], ((g / kAStages) & 1u) ^ 1u, err);
+                uint32_t s0, s1, r[16];
+                scale_pairs(sc4 & 0xFFFFu, s0, s1);
+                decode8(c0.x, s0, r);
+                decode8(c0.y, s0, r + 4);
+                decode8(c0.z, s1, r + 8);
+                decode8(c0.w, s1, r + 12);
+                ok = wait_warp(sm, &sm.empty[s], ph ^ 1u, err);
                 if (!ok) break;
                 tc_after();
-                tmem_st16(acol + sa * 32u, r);
-                tmem_st16(acol + sa * 32u + 16u, r + 16);
+                tmem_st16(acol + s * 32u, r);
+                scale_pairs(sc4 >> 16, s0, s1);
+                decode8(c1.x, s0, r);
+                decode8(c1.y, s0, r + 4);
+                decode8(c1.z, s1, r + 8);
+                decode8(c1.w, s1, r + 12);
+                tmem_st16(acol + s * 32u + 16u, r);
+                ok = wait_warp(sm, &sm.bfull[s], ph, err);   // the issuer then waits for one barrier
+                if (!ok) break;
                 tc_wait_st();
                 tc_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.afull[sa]);
+                if (lane == 0) mbar_arrive(&sm.ready[s]);
+                sc += kDqGroups;
+                if (sc >= kCStages) { sc -= kCStages; pc ^= 1u; }
+                s += kDqGroups;
+                if (s >= kStages) { s -= kStages; ph ^= 1u; }
             }
+            skip = kt - it.k1;                   // of the next item's first stages
         }
-    } else if (warp >= kEpiWarp0) {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
         const int eg = (warp - kEpiWarp0) >> 2, q = (warp & 3) * 32 + lane;
-        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const float g0 = __ldg(a.ep.global0) * 0x1p14f, g1 = a.ep.act == TFMOE_ACT_SWIGLU ? __ldg(a.ep.global1) * 0x1p14f : 0.f;
+        const uint32_t d = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const float g0 = __ldg(a.ep.global0) * 0x1p14f, g1 = Act == TFMOE_ACT_SWIGLU ? __ldg(a.ep.global1) * 0x1p14f : 0.f;
         grid_dep_wait();
         uint32_t n_item = 0;
         for (int i = blockIdx.x; i < a.items; i += gridDim.x, ++n_item) {
             const Item it(a, i);
-            const int buf = (int)(n_item % kDBufs);
             const int steps = (min(a.N, a.T - it.t0) + 15) >> 4;
             // after an abort a split item's warps still meet at the barriers below, and read nothing
-            const bool ok = wait_warp(sm, &sm.dfull[buf], (n_item / kDBufs) & 1u, err);
+            const bool ok = wait_warp(sm, &sm.dfull, n_item & 1u, err);
             if (!ok && a.splits == 1) break;
-            tc_after();
-            const uint32_t d = tmem + lane_base + (uint32_t)buf * kMaxN;
-            float *mine = a.partial + (size_t)i * a.N * kM + q;
-            for (int st = ok ? eg : steps; st < steps; st += kEpiGroups) {
-                uint32_t r[16];
-                tmem_ld16(d + (uint32_t)(st * 16), r);
-                tc_wait_ld();
-                if (st + kEpiGroups >= steps) {  // the warp's last read of the accumulator
-                    tc_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.dempty[buf]);
-                }
-                if (a.splits == 1) {
-                    finish16(a, it.rt, q, it.t0 + st * 16, g0, g1, [&](int j) { return __uint_as_float(r[j]); });
-                } else {
+            uint32_t r[kHeld][16];
+            if (ok) {
+                tc_after();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) mine[(size_t)(st * 16 + j) * kM] = __uint_as_float(r[j]);
-                }
-            }
-            if (ok && eg >= steps) {
+                for (int j = 0; j < kHeld; ++j)
+                    if (2 * j + eg < steps) tmem_ld16(d + (uint32_t)(16 * (2 * j + eg)), r[j]);
+                tc_wait_ld();
                 tc_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.dempty[buf]);
+                if (lane == 0) mbar_arrive(&sm.dempty);
             }
-            if (a.splits == 1) continue;
-            epilogue_sync();
-            if (threadIdx.x == kEpiWarp0 * 32) {
-                __threadfence();                 // the CTA's sums, ordered by the barrier
-                const int last = atomicAdd(a.tickets + it.tile, 1) == a.splits - 1;
-                if (last) a.tickets[it.tile] = 0;
-                __threadfence();
-                sm.is_last = last;
-            }
-            epilogue_sync();
-            if (sm.is_last) {
+            if (a.splits > 1) {
+                float *mine = a.partial + (size_t)i * a.N * kM + q;
+#pragma unroll
+                for (int j = 0; j < kHeld; ++j)
+                    if (ok && 2 * j + eg < steps)
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) mine[(size_t)(16 * (2 * j + eg) + c) * kM] = __uint_as_float(r[j][c]);
+                epilogue_sync();
+                if (threadIdx.x == kEpiWarp0 * 32) {
+                    __threadfence();             // the CTA's sums, ordered by the barrier
+                    const int last = atomicAdd(a.tickets + it.tile, 1) == a.splits - 1;
+                    if (last) a.tickets[it.tile] = 0;
+                    __threadfence();
+                    sm.is_last = last;
+                }
+                epilogue_sync();
+                const bool last = sm.is_last;
+                epilogue_sync();                 // is_last is free again
+                if (!last) continue;
                 const float *src = a.partial + (size_t)it.tile * a.splits * a.N * kM + q;
                 const size_t stride = (size_t)a.N * kM;
-                for (int st = eg; st < steps; st += kEpiGroups) {
-                    float v[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = __ldcg(src + (size_t)(st * 16 + j) * kM);
-                    for (int s = 1; s < a.splits; ++s) {
+                for (int j = 0; j < kHeld; ++j) {
+                    if (2 * j + eg >= steps) continue;
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) r[j][c] = __float_as_uint(__ldcg(src + (size_t)(16 * (2 * j + eg) + c) * kM));
+                }
+                for (int sp = 1; sp < a.splits; ++sp) {
+                    src += stride;
+#pragma unroll
+                    for (int j = 0; j < kHeld; ++j) {
+                        if (2 * j + eg >= steps) continue;
                         float u[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) u[j] = __ldcg(src + s * stride + (size_t)(st * 16 + j) * kM);
+                        for (int c = 0; c < 16; ++c) u[c] = __ldcg(src + (size_t)(16 * (2 * j + eg) + c) * kM);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] += u[j];
+                        for (int c = 0; c < 16; ++c) r[j][c] = __float_as_uint(__uint_as_float(r[j][c]) + u[c]);
                     }
-                    finish16(a, it.rt, q, it.t0 + st * 16, g0, g1, [&](int j) { return v[j]; });
                 }
             }
-            epilogue_sync();                     // is_last is free again
+            finish_held<Act, Fast>(a, it.rt, q, it.t0, eg, steps, g0, g1, r);
         }
     }
     __syncthreads();
@@ -393,6 +475,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     }
 }
 
+using TcKernel = void (*)(const CUtensorMap, const TcArgs);
+template <bool Fast>
+TcKernel tc_kernel(int act) {
+    switch (act) {
+    case TFMOE_ACT_RELU: return linear_tc_kernel<TFMOE_ACT_RELU, Fast>;
+    case TFMOE_ACT_SILU: return linear_tc_kernel<TFMOE_ACT_SILU, Fast>;
+    case TFMOE_ACT_GELU: return linear_tc_kernel<TFMOE_ACT_GELU, Fast>;
+    case TFMOE_ACT_GELU_TANH: return linear_tc_kernel<TFMOE_ACT_GELU_TANH, Fast>;
+    case TFMOE_ACT_SWIGLU: return linear_tc_kernel<TFMOE_ACT_SWIGLU, Fast>;
+    default: return linear_tc_kernel<TFMOE_ACT_NONE, Fast>;
+    }
+}
+TcKernel tc_kernel(const Linear &L) {
+    return L.desc.flags & TFMOE_FLAG_OUT_FP32 ? tc_kernel<false>(L.desc.activation) : tc_kernel<true>(L.desc.activation);
+}
+
 constexpr size_t kSmemBytes = sizeof(TcSmem) + 1024;
 
 struct TcPlan {
@@ -400,8 +498,8 @@ struct TcPlan {
 };
 
 // The tile width and the number of splits with the least estimated time, in clocks of an SM. A stage of 64
-// columns takes its MMAs' time, or the decode's where N is small; a wave ends with its last epilogue
-// (about 6 clocks an output of the 128 rows); splits add the sums' way to global memory and back.
+// columns takes its MMAs' time or, where N is small, that of issuing them; a launch ends with its last
+// epilogue (about 30 clocks a token); splits add the sums' way to global memory and back.
 TcPlan make_tc_plan(const Linear &L, int T) {
     TcPlan best{16, 1};
     double least = 1e30;
@@ -410,8 +508,8 @@ TcPlan make_tc_plan(const Linear &L, int T) {
         for (int S = 1; S <= kMaxSplits && S <= L.KT; ++S) {
             if (S > 1 && tiles * S > L.num_sms) break;         // the workspace holds one wave of sums
             const int64_t waves = (tiles * S + L.num_sms - 1) / L.num_sms;
-            const double stage = std::max(2.0 * N, 230.0), stages = (double)((L.KT + S - 1) / S);
-            double t = (double)waves * stages * stage + 6.0 * N + 3000.0;
+            const double stage = std::max(2.0 * N, 400.0), stages = (double)((L.KT + S - 1) / S);
+            double t = (double)waves * (stages * stage + 600.0) + 30.0 * N + 3000.0;
             if (S > 1) t += 3000.0 + 10.0 * N + 8.0 * N * S;
             if (t < least) { least = t; best = {N, S}; }
         }
@@ -422,9 +520,9 @@ TcPlan make_tc_plan(const Linear &L, int T) {
 
 }  // namespace
 
-cudaError_t linear_tc_setup(const Linear &)
+cudaError_t linear_tc_setup(const Linear &L)
 {
-    return cudaFuncSetAttribute(linear_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    return cudaFuncSetAttribute(tc_kernel(L), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
 }
 
 size_t linear_tc_partial_floats(const Linear &L) {
@@ -457,7 +555,7 @@ cudaError_t launch_linear_tc(Linear &L, const uint16_t *x, int64_t ldx, int T, c
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_tc_kernel, map, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, tc_kernel(L), map, a);
     *launches += 1;
     return e != cudaSuccess ? e : cudaGetLastError();
 }
