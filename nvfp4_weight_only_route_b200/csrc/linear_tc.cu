@@ -1,7 +1,7 @@
 // linear_tc.cu -- the tensor-core regime of the NVFP4 matrix product: more tokens than the streaming
 // regime takes, bound by the bf16 tensor pipe (large T) or by latency (short prompts).
 //
-// A tile is 128 weight rows (MMA M) x N <= 224 tokens (MMA N), the reduction in stages of 64. The weights are
+// A tile is 128 weight rows (MMA M) x N <= 192 tokens (MMA N), the reduction in stages of 64. The weights are
 // decoded to bf16 in registers and stored into tensor memory as the A operand; the bf16 token rows
 // come by TMA (128-byte swizzle) into shared memory as the B operand: no rounding of either. Per CTA
 // (one per SM, 24 warps):
@@ -10,25 +10,31 @@
 //   warp 1       owns tensor memory, issues four MMAs of K = 16 per stage
 //   warps 4-15   three decode warpgroups taking every third stage, a thread per weight row
 //   warps 16-23  epilogue, two warpgroups taking alternate 16-token steps of the accumulator
-// Tensor memory: the accumulator at columns [0, 224), five decoded stages of 32 columns from 256.
+// Tensor memory: two accumulators of 192 columns, so that a tile's epilogue runs under the next tile's
+// products, and four decoded stages of 32 columns: all 512.
 //
-// What bounds the main loop is the issue: four MMAs, a commit and a barrier wait cost the issuing warp about
-// 460 clocks (two accumulators of 192 columns, 384 clocks of MMA per stage, ran at 680 with two waits
-// and two commits), so a stage's decoders wait for its token tile too, one barrier and one commit
-// serve both operands, the next stage's barrier is asked before the current MMAs are issued, and the
-// tile is as wide as the epilogue can take out of tensor memory at once: its 256 threads load the whole
-// accumulator into registers (up to 112 each), hand it back within a few hundred clocks, and finish
-// the tile under the next one's products. The register split follows from that: 144 for the epilogue,
-// 48 for the others.
+// What bounds the main loop is the issue: four MMAs, a commit and a barrier wait keep the issuing warp
+// about 380 clocks, as long as a stage's MMAs take at N = 192 (two waits and two commits: 680). So a
+// stage's decoders wait for its token tile too, one barrier tells the issuer of both operands, one commit
+// frees both (the A slot of stage g, a quarter of a shorter ring, was stage g - 4's), and the next
+// stage's barrier is asked while the current MMAs are issued. (One accumulator of 224 columns that the
+// epilogue takes into 112 registers a thread at once was as fast at 7234 tokens, but its 50 KB of
+// straight-line code came from memory in every launch: 28 us against 16 at 601 tokens.)
 //
-// The decode: a stage must be decoded in the time of its MMAs (2 N clocks, 416 at N = 208). A conversion
+// Measured: 7234 x 4096 x 2 x 2688 with SwiGLU 248 us (1.29 PFLOP/s, 0.78 of the measured bf16 rate); the
+// tensor pipe works in 61 % of the cycles. The decode and the epilogue take most of the rest: with the
+// decode's arithmetic left out 212 us, without the epilogue's as well 203. 601 x 2688 x 1001 16.4 us,
+// 100 x 1536 x 4096 10.8.
+//
+// The decode: a stage must be decoded in the time of its MMAs (2 N clocks, 384 at N = 192). A conversion
 // to f16 and on to bf16 would take about 410 clocks per stage of an SM's conversion rate (36 lanes per clock
 // for E2M1, 63 for f16 -> f32). So the code's bits are placed instead: sign at bit 15 and the three
 // magnitude bits at 8..6 of a bf16 are that E2M1 value times 2^-126, its subnormal included; one
 // bf16x2 multiplication by the block scale times 2^112 gives value * scale * 2^-14 exactly (at most 6
 // significant bits, 2^-24 to 0.17), and 2^14 joins the multiplier in the epilogue. The tiled layout
 // keeps the eight codes of a word in the order 0 2 4 6 1 3 5 7, so that a shift brings the codes of
-// columns 2j and 2j + 1 to the same place of both halves.
+// columns 2j and 2j + 1 to the same place of both halves; a product by 2^6 + 2^12 puts magnitude and sign
+// where they belong in one instruction, which the integer multiplier does beside the logic unit.
 //
 // Few tiles leave SMs idle, so their reductions are split: CTA (tile, split) leaves its sums in global memory,
 // and the CTA that arrives last at the tile's counter adds them in split order and finishes the tile.
@@ -43,29 +49,25 @@ namespace tfmoe {
 namespace {
 
 constexpr int kM = 128;
-constexpr int kMaxN = 224;
-constexpr int kStages = 5, kCStages = 12;
+constexpr int kMaxN = 192;
+constexpr int kStages = 6, kAStages = 4, kCStages = 12, kDBufs = 2;
 constexpr int kDqGroups = 3, kEpiGroups = 2;
 constexpr int kDqWarp0 = 4, kEpiWarp0 = kDqWarp0 + 4 * kDqGroups;
 constexpr int kThreads = 32 * (kEpiWarp0 + 4 * kEpiGroups);
 constexpr int kEpiThreads = 128 * kEpiGroups;
-constexpr int kHeld = kMaxN / 16 / kEpiGroups;       // 16-token steps an epilogue thread holds
-constexpr uint32_t kACol = 256, kTmemCols = 512;
-static_assert(kMaxN <= (int)kACol && kACol + kStages * 32 <= kTmemCols, "tensor memory");
-static_assert(kMaxN % (16 * kEpiGroups) == 0, "even share of the steps");
+constexpr uint32_t kACol = kDBufs * kMaxN, kTmemCols = 512;
+static_assert(kACol + kAStages * 32 <= kTmemCols, "tensor memory");
+static_assert(kAStages < kStages, "an A slot's last use is told by the barrier of its stage");
 constexpr int kBBytes = kMaxN * 128;
 constexpr int kMaxSplits = 8;
-// 768 threads start with 80 registers (61440 in all).
-constexpr int kEpiRegs = 144, kOtherRegs = 48;
-static_assert(kEpiThreads * kEpiRegs + (kThreads - kEpiThreads) * kOtherRegs <= kThreads * 80, "register split");
 
 struct TcSmem {
     uint8_t b[kStages][kBBytes];             // 1024-byte aligned
     uint8_t codes[kCStages][kTileCodeBytes];
     uint8_t scales[kCStages][kTileScaleBytes];
-    uint64_t bfull[kStages], ready[kStages], empty[kStages];
+    uint64_t bfull[kStages], ready[kStages], done[kStages];   // token tile landed; both operands there; MMAs complete
     uint64_t cfull[kCStages], cempty[kCStages];
-    uint64_t dfull, dempty;
+    uint64_t dfull[kDBufs], dempty[kDBufs];
     uint64_t mma_done;
     uint32_t tmem_base;
     int32_t abort_flag;
@@ -158,9 +160,11 @@ __device__ __forceinline__ void scale_pairs(uint32_t two, uint32_t &lo, uint32_t
 }
 // Eight codes (order 0 2 4 6 1 3 5 7) times the scale pair -> four bf16x2, columns in order.
 __device__ __forceinline__ void decode8(uint32_t w, uint32_t scale, uint32_t *o) {
-    constexpr uint32_t kSign = 0x80008000u, kMag = 0x01C001C0u;
-    const uint32_t v[4] = {((w << 12) & kSign) | ((w << 6) & kMag), ((w << 8) & kSign) | ((w << 2) & kMag),
-                           ((w << 4) & kSign) | ((w >> 2) & kMag), (w & kSign) | ((w >> 6) & kMag)};
+    constexpr uint32_t kKeep = 0x81C081C0u;
+    const uint32_t w8 = w >> 8;
+    // a code times 2^6 + 2^12: its magnitude at bits 8..6, its sign at bit 15, and copies that the mask drops
+    const uint32_t v[4] = {(w & 0x000F000Fu) * 4160u & kKeep, (w & 0x00F000F0u) * 260u & kKeep,
+                           (w8 & 0x000F000Fu) * 4160u & kKeep, (w8 & 0x00F000F0u) * 260u & kKeep};
 #pragma unroll
     for (int j = 0; j < 4; ++j) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[j]) : "r"(v[j]), "r"(scale));
 }
@@ -191,58 +195,69 @@ __device__ __forceinline__ float activate_fast(float y, int act) {
     }
 }
 
-// The held sums of one epilogue thread: step j is tokens t0 + 16 (2 j + eg) .. + 15 of this lane's weight row.
+// One epilogue thread's place: its output column and where its next step's tokens lie.
 template <int Act, bool Fast>
-__device__ __forceinline__ void finish_held(const TcArgs &a, int rt, int q, int t0, int eg, int steps, float g0, float g1,
-                                            const uint32_t (&r)[kHeld][16]) {
-    const LinearEpilogue &ep = a.ep;
-    auto act = [&](float y) { return Fast ? activate_fast(y, Act) : activate(y, Act); };
-    if (Act == TFMOE_ACT_SWIGLU) {
-        // an even lane has gate row j of the 16 tokens, the odd lane after it up row j: the even lane finishes
-        // tokens 0..7, the odd one 8..15
-        const bool odd = q & 1;
-        const int n = (rt * kM + q) >> 1;
-        const float b0 = ep.bias && n < ep.N ? __ldg(ep.bias + n) : 0.f, b1 = ep.bias && n < ep.N ? __ldg(ep.bias + ep.N + n) : 0.f;
+struct Finisher {
+    static constexpr bool kGated = Act == TFMOE_ACT_SWIGLU;
+    static constexpr int kTok = kGated ? 8 : 16;   // tokens of a step that this lane finishes
+    const LinearEpilogue &ep;
+    int T, t;                                      // the call's tokens; the step's first one of this lane
+    bool odd, in;
+    float g0, g1, b0, b1;
+    const uint16_t *res;
+    char *out;
+
+    // gated: an even lane has gate row j of a step's 16 tokens, the odd lane after it up row j; the even lane
+    // finishes tokens 0..7, the odd one 8..15
+    __device__ __forceinline__ Finisher(const LinearEpilogue &e, int tokens, int rt, int q, int first, float m0, float m1)
+        : ep(e), T(tokens), odd(kGated && (q & 1)), g0(m0), g1(m1) {
+        const int n = kGated ? (rt * kM + q) >> 1 : rt * kM + q;
+        in = n < ep.N;
+        b0 = ep.bias && in ? __ldg(ep.bias + n) : 0.f;
+        b1 = kGated && ep.bias && in ? __ldg(ep.bias + ep.N + n) : 0.f;
+        t = first + (odd ? 8 : 0);
+        res = ep.residual ? ep.residual + (int64_t)t * ep.ldr + n : nullptr;
+        out = static_cast<char *>(ep.out) + ((int64_t)t * ep.ldo + n) * (Fast ? 2 : 4);
+    }
+    // A step's 16 sums of this lane's weight row; the next step is 16 kEpiGroups tokens on. The residual is
+    // loaded for eight tokens before any of them is stored: out may be the residual, so the compiler moves no
+    // load ahead of a store, and one load at a time would cost its latency per token.
+    __device__ __forceinline__ void step(const uint32_t (&s)[16]) {
+        const int64_t ob = ep.ldo * (Fast ? 2 : 4);
 #pragma unroll
-        for (int j = 0; j < kHeld; ++j) {
-            if (2 * j + eg >= steps) continue;
-            const int t = t0 + 16 * (2 * j + eg) + (odd ? 8 : 0);
-            const uint16_t *res = ep.residual ? ep.residual + (int64_t)t * ep.ldr + n : nullptr;
-            char *out = static_cast<char *>(ep.out) + ((int64_t)t * ep.ldo + n) * (Fast ? 2 : 4);
+        for (int h = 0; h < kTok; h += 8) {
+            uint32_t rv[8];
+            if (res) {
+                const uint16_t *p = res;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float lo = __uint_as_float(r[j][i]), hi = __uint_as_float(r[j][i + 8]);
-                const float keep = odd ? hi : lo, got = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
-                const float gate = fmaf(odd ? got : keep, g0, b0), up = fmaf(odd ? keep : got, g1, b1);
-                if (t + i < a.T && n < ep.N) {
-                    float v = (Fast ? silu_f32(gate) : activate(gate, TFMOE_ACT_SILU)) * up;
-                    if (res) v += bf16_bits_to_float(res[i * ep.ldr]);
-                    if (Fast) *reinterpret_cast<uint16_t *>(out + i * ep.ldo * 2) = float_to_bf16_bits_rn(v);
-                    else *reinterpret_cast<float *>(out + i * ep.ldo * 4) = v;
+                for (int i = 0; i < 8; ++i, p += ep.ldr) rv[i] = in && t + i < T ? *p : 0u;
+            }
+            char *p = out;
+#pragma unroll
+            for (int i = 0; i < 8; ++i, p += ob) {
+                float v;
+                if (kGated) {
+                    const float lo = __uint_as_float(s[i]), hi = __uint_as_float(s[i + 8]);
+                    const float keep = odd ? hi : lo, got = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+                    const float gate = fmaf(odd ? got : keep, g0, b0), up = fmaf(odd ? keep : got, g1, b1);
+                    v = (Fast ? silu_f32(gate) : activate(gate, TFMOE_ACT_SILU)) * up;
+                } else {
+                    const float y = fmaf(__uint_as_float(s[h + i]), g0, b0);
+                    v = Fast ? activate_fast(y, Act) : activate(y, Act);
+                }
+                if (res) v += bf16_bits_to_float(rv[i]);
+                if (in && t + i < T) {
+                    if (Fast) *reinterpret_cast<uint16_t *>(p) = float_to_bf16_bits_rn(v);
+                    else *reinterpret_cast<float *>(p) = v;
                 }
             }
-        }
-    } else {
-        const int n = rt * kM + q;
-        if (n >= ep.N) return;
-        const float b0 = ep.bias ? __ldg(ep.bias + n) : 0.f;
-#pragma unroll
-        for (int j = 0; j < kHeld; ++j) {
-            if (2 * j + eg >= steps) continue;
-            const int t = t0 + 16 * (2 * j + eg);
-            const uint16_t *res = ep.residual ? ep.residual + (int64_t)t * ep.ldr + n : nullptr;
-            char *out = static_cast<char *>(ep.out) + ((int64_t)t * ep.ldo + n) * (Fast ? 2 : 4);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (t + i >= a.T) break;
-                float v = act(fmaf(__uint_as_float(r[j][i]), g0, b0));
-                if (res) v += bf16_bits_to_float(res[i * ep.ldr]);
-                if (Fast) *reinterpret_cast<uint16_t *>(out + i * ep.ldo * 2) = float_to_bf16_bits_rn(v);
-                else *reinterpret_cast<float *>(out + i * ep.ldo * 4) = v;
-            }
+            const int ahead = h + 8 < kTok ? 8 : 16 * kEpiGroups + 8 - kTok;
+            if (res) res += ahead * ep.ldr;
+            out += ahead * ob;
+            t += ahead;
         }
     }
-}
+};
 
 template <int Act, bool Fast>
 __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_constant__ CUtensorMap xmap, const TcArgs a)
@@ -251,10 +266,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     TcSmem &sm = *reinterpret_cast<TcSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) { mbar_init(&sm.bfull[s], 1); mbar_init(&sm.ready[s], 4); mbar_init(&sm.empty[s], 1); }
+        for (int s = 0; s < kStages; ++s) { mbar_init(&sm.bfull[s], 1); mbar_init(&sm.ready[s], 4); mbar_init(&sm.done[s], 1); }
         for (int s = 0; s < kCStages; ++s) { mbar_init(&sm.cfull[s], 1); mbar_init(&sm.cempty[s], 4); }
-        mbar_init(&sm.dfull, 1);
-        mbar_init(&sm.dempty, 4 * kEpiGroups);
+        for (int s = 0; s < kDBufs; ++s) { mbar_init(&sm.dfull[s], 1); mbar_init(&sm.dempty[s], 4 * kEpiGroups); }
         mbar_init(&sm.mma_done, 1);
         sm.abort_flag = 0;
         fence_mbar_init();
@@ -271,13 +285,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     const uint32_t tmem = sm.tmem_base;
     int32_t *err = a.err_word;
 
-    if (warp < kDqWarp0) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-      if (warp == 0 || warp == 2) {
+    if (warp == 0 || warp == 2) {
         if (lane == 0) {
             const bool tokens = warp == 0;
             const int nst = tokens ? kStages : kCStages;
-            uint64_t *full = tokens ? sm.bfull : sm.cfull, *empty = tokens ? sm.empty : sm.cempty;
+            uint64_t *full = tokens ? sm.bfull : sm.cfull, *empty = tokens ? sm.done : sm.cempty;
             if (tokens) grid_dep_wait();         // the weights are nobody's output; the tokens may be
             uint32_t issued = 0, ph = 0;
             int s = 0;
@@ -309,18 +321,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 }
             }
         }
-      } else if (warp == 1) {
+    } else if (warp == 1) {
         const uint64_t bdesc0 = smem_desc(smem_u32(sm.b[0]));
         int s = 0;
-        uint32_t ph = 0, n_item = 0;
+        uint32_t ph = 0, n_item = 0, g = 0;
         bool ok = true;
         for (int i = blockIdx.x; i < a.items && ok; i += gridDim.x, ++n_item) {
             const Item it(a, i);
             const uint32_t idesc = instr_desc(min(a.N, (a.T - it.t0 + 15) & ~15));
-            ok = wait_warp(sm, &sm.dempty, (n_item & 1u) ^ 1u, err);
+            const int buf = (int)(n_item % kDBufs);
+            ok = wait_warp(sm, &sm.dempty[buf], ((n_item / kDBufs) & 1u) ^ 1u, err);
             if (!ok) break;
+            const uint32_t d = tmem + (uint32_t)buf * kMaxN;
             bool here = test_now(&sm.ready[s], ph);
-            for (int kt = it.k0; kt < it.k1; ++kt) {
+            for (int kt = it.k0; kt < it.k1; ++kt, ++g) {
                 if (!__all_sync(0xffffffffu, here)) {
                     ok = wait_warp(sm, &sm.ready[s], ph, err);
                     if (!ok) break;
@@ -332,32 +346,30 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 here = test_now(&sm.ready[sn], pn);
                 if (elect_one()) {
                     const uint64_t bd = bdesc0 + (uint64_t)(s * (kBBytes >> 4));
-                    const uint32_t ad = tmem + kACol + (uint32_t)s * 32u;
-                    mma_ts(tmem, ad, bd, idesc, kt != it.k0);
-                    mma_ts(tmem, ad + 8u, bd + 2u, idesc, 1u);
-                    mma_ts(tmem, ad + 16u, bd + 4u, idesc, 1u);
-                    mma_ts(tmem, ad + 24u, bd + 6u, idesc, 1u);
-                    commit(&sm.empty[s]);
+                    const uint32_t ad = tmem + kACol + (g % kAStages) * 32u;
+                    mma_ts(d, ad, bd, idesc, kt != it.k0);
+                    mma_ts(d, ad + 8u, bd + 2u, idesc, 1u);
+                    mma_ts(d, ad + 16u, bd + 4u, idesc, 1u);
+                    mma_ts(d, ad + 24u, bd + 6u, idesc, 1u);
+                    commit(&sm.done[s]);
                 }
                 __syncwarp();
                 s = sn;
                 ph = pn;
             }
             if (!ok) break;
-            if (elect_one()) commit(&sm.dfull);
+            if (elect_one()) commit(&sm.dfull[buf]);
             __syncwarp();
         }
         // on every path: tensor memory and the stages stay in use until the MMAs issued are complete
         if (elect_one()) commit(&sm.mma_done);
         __syncwarp();
-      }
-    } else if (warp < kEpiWarp0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    } else if (warp >= kDqWarp0 && warp < kEpiWarp0) {
         const int gq = (warp - kDqWarp0) >> 2, q = (warp & 3) * 32 + lane;
         const uint32_t acol = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kACol;
-        // this group's stages are the running numbers gq, gq + 3, ...
-        int skip = gq;
-        uint32_t sc = gq % kCStages, pc = 0, s = gq % kStages, ph = 0;
+        // this group's stages are the running numbers gq, gq + 3, ...; ring places are kept, not divided for
+        int sc = gq, s = gq, sa = gq, skip = gq;
+        uint32_t pc = 0, ps = 0;
         bool ok = true;
         for (int i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
             const Item it(a, i);
@@ -370,37 +382,35 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 const uint32_t sc4 = *reinterpret_cast<const uint32_t *>(sm.scales[sc] + q * 4);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.cempty[sc]);
-                uint32_t s0, s1, r[16];
-                scale_pairs(sc4 & 0xFFFFu, s0, s1);
-                decode8(c0.x, s0, r);
-                decode8(c0.y, s0, r + 4);
-                decode8(c0.z, s1, r + 8);
-                decode8(c0.w, s1, r + 12);
-                ok = wait_warp(sm, &sm.empty[s], ph ^ 1u, err);
+                uint32_t sp[4], r[32];
+                scale_pairs(sc4 & 0xFFFFu, sp[0], sp[1]);
+                scale_pairs(sc4 >> 16, sp[2], sp[3]);
+                const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+                for (int w = 0; w < 8; ++w) decode8(words[w], sp[w >> 1], r + 4 * w);
+                // the A slot was stage g - 4's, kStages - 4 places on in the ring: its MMAs are complete (the
+                // barrier's next phase, stage g + 2's, cannot end before this stage is decoded; stages 0..3 find the
+                // phase before the first complete)
+                const int sd = s + kStages - kAStages < kStages ? s + kStages - kAStages : s - kAStages;
+                ok = wait_warp(sm, &sm.done[sd], sd > s ? ps ^ 1u : ps, err);
                 if (!ok) break;
                 tc_after();
-                tmem_st16(acol + s * 32u, r);
-                scale_pairs(sc4 >> 16, s0, s1);
-                decode8(c1.x, s0, r);
-                decode8(c1.y, s0, r + 4);
-                decode8(c1.z, s1, r + 8);
-                decode8(c1.w, s1, r + 12);
-                tmem_st16(acol + s * 32u + 16u, r);
-                ok = wait_warp(sm, &sm.bfull[s], ph, err);   // the issuer then waits for one barrier
+                const uint32_t col = acol + (uint32_t)sa * 32u;
+                tmem_st16(col, r);
+                tmem_st16(col + 16u, r + 16);
+                ok = wait_warp(sm, &sm.bfull[s], ps, err);
                 if (!ok) break;
                 tc_wait_st();
                 tc_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.ready[s]);
-                sc += kDqGroups;
-                if (sc >= kCStages) { sc -= kCStages; pc ^= 1u; }
-                s += kDqGroups;
-                if (s >= kStages) { s -= kStages; ph ^= 1u; }
+                if ((sc += kDqGroups) >= kCStages) { sc -= kCStages; pc ^= 1u; }
+                if ((s += kDqGroups) >= kStages) { s -= kStages; ps ^= 1u; }
+                if ((sa += kDqGroups) >= kAStages) sa -= kAStages;
             }
             skip = kt - it.k1;                   // of the next item's first stages
         }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+    } else if (warp >= kEpiWarp0) {
         const int eg = (warp - kEpiWarp0) >> 2, q = (warp & 3) * 32 + lane;
         const uint32_t d = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float g0 = __ldg(a.ep.global0) * 0x1p14f, g1 = Act == TFMOE_ACT_SWIGLU ? __ldg(a.ep.global1) * 0x1p14f : 0.f;
@@ -410,26 +420,31 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             const Item it(a, i);
             const int steps = (min(a.N, a.T - it.t0) + 15) >> 4;
             // after an abort a split item's warps still meet at the barriers below, and read nothing
-            const bool ok = wait_warp(sm, &sm.dfull, n_item & 1u, err);
+            const int buf = (int)(n_item % kDBufs);
+            const bool ok = wait_warp(sm, &sm.dfull[buf], (n_item / kDBufs) & 1u, err);
             if (!ok && a.splits == 1) break;
-            uint32_t r[kHeld][16];
-            if (ok) {
-                tc_after();
-#pragma unroll
-                for (int j = 0; j < kHeld; ++j)
-                    if (2 * j + eg < steps) tmem_ld16(d + (uint32_t)(16 * (2 * j + eg)), r[j]);
+            tc_after();
+            const uint32_t dcol = d + (uint32_t)buf * kMaxN;
+            auto load = [&](int st, uint32_t (&r)[16]) {
+                tmem_ld16(dcol + (uint32_t)(16 * st), r);
                 tc_wait_ld();
-                tc_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.dempty);
-            }
+                if (st + kEpiGroups >= steps) {  // the warp's last read of the accumulator
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.dempty[buf]);
+                }
+            };
+            if (ok && eg >= steps && lane == 0) mbar_arrive(&sm.dempty[buf]);
             if (a.splits > 1) {
-                float *mine = a.partial + (size_t)i * a.N * kM + q;
+                float *mine = a.partial + ((size_t)i * a.N + 16 * eg) * kM + q;
+#pragma unroll 1
+                for (int st = ok ? eg : steps; st < steps; st += kEpiGroups) {
+                    uint32_t r[16];
+                    load(st, r);
 #pragma unroll
-                for (int j = 0; j < kHeld; ++j)
-                    if (ok && 2 * j + eg < steps)
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) mine[(size_t)(16 * (2 * j + eg) + c) * kM] = __uint_as_float(r[j][c]);
+                    for (int c = 0; c < 16; ++c) mine[c * kM] = __uint_as_float(r[c]);
+                    mine += 16 * kEpiGroups * kM;
+                }
                 epilogue_sync();
                 if (threadIdx.x == kEpiWarp0 * 32) {
                     __threadfence();             // the CTA's sums, ordered by the barrier
@@ -442,28 +457,29 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 const bool last = sm.is_last;
                 epilogue_sync();                 // is_last is free again
                 if (!last) continue;
-                const float *src = a.partial + (size_t)it.tile * a.splits * a.N * kM + q;
-                const size_t stride = (size_t)a.N * kM;
+            }
+            Finisher<Act, Fast> fin(a.ep, a.T, it.rt, q, it.t0 + 16 * eg, g0, g1);
+            const float *src = a.partial + ((size_t)it.tile * a.splits * a.N + 16 * eg) * kM + q;
+#pragma unroll 1
+            for (int st = eg; st < steps; st += kEpiGroups) {
+                uint32_t r[16];
+                if (a.splits == 1) {
+                    load(st, r);
+                } else {
 #pragma unroll
-                for (int j = 0; j < kHeld; ++j) {
-                    if (2 * j + eg >= steps) continue;
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) r[j][c] = __float_as_uint(__ldcg(src + (size_t)(16 * (2 * j + eg) + c) * kM));
-                }
-                for (int sp = 1; sp < a.splits; ++sp) {
-                    src += stride;
-#pragma unroll
-                    for (int j = 0; j < kHeld; ++j) {
-                        if (2 * j + eg >= steps) continue;
+                    for (int c = 0; c < 16; ++c) r[c] = __float_as_uint(__ldcg(src + c * kM));
+#pragma unroll 1
+                    for (int sp = 1; sp < a.splits; ++sp) {
                         float u[16];
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) u[c] = __ldcg(src + (size_t)(16 * (2 * j + eg) + c) * kM);
+                        for (int c = 0; c < 16; ++c) u[c] = __ldcg(src + ((size_t)sp * a.N + c) * kM);
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) r[j][c] = __float_as_uint(__uint_as_float(r[j][c]) + u[c]);
+                        for (int c = 0; c < 16; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) + u[c]);
                     }
+                    src += 16 * kEpiGroups * kM;
                 }
+                fin.step(r);
             }
-            finish_held<Act, Fast>(a, it.rt, q, it.t0, eg, steps, g0, g1, r);
         }
     }
     __syncthreads();
