@@ -202,7 +202,7 @@ TFMOE_API tfmoe_status tfmoe_forward_add_norm(tfmoe_layer *layer, const uint16_t
  *    the call writes LOGITS (every entry exact), TOPK_IDS and TOPK_WEIGHTS; the others hold
  *    what an earlier forward left, and tfmoe_forward_stage has nothing to replay after it.
  * TFMOE_ERR_UNSUPPORTED when T is above tfmoe_decode_max_tokens(layer): the token operands
- * have to fit in shared memory, which takes rows of hidden or intermediate above about 4800
+ * have to fit in shared memory, which takes rows of hidden or intermediate above about 4400
  * elements down from 16 tokens.
  * The device-side waits are bounded; when one gives up, the output is undefined and
  * tfmoe_sync_status reports TFMOE_ERR_TIMEOUT.
