@@ -6,7 +6,7 @@
 // come by TMA (128-byte swizzle) into shared memory as the B operand: no rounding of either. Per CTA
 // (one per SM, 24 warps):
 //   warp 0       token tiles (TMA) into a ring that the MMA commits free
-//   warp 2       codes and scales (bulk copies) into a ring that the decoders free
+//   warp 2       codes and scales of four stages at a time (two bulk copies) into a ring that the decoders free
 //   warp 1       owns tensor memory, issues four MMAs of K = 16 per stage
 //   warps 4-15   three decode warpgroups taking every third stage, a thread per weight row
 //   warps 16-23  epilogue, two warpgroups taking alternate 16-token steps of the accumulator
@@ -50,7 +50,8 @@ namespace {
 
 constexpr int kM = 128;
 constexpr int kMaxN = 192;
-constexpr int kStages = 6, kAStages = 4, kCStages = 12, kDBufs = 2;
+constexpr int kStages = 6, kAStages = 4, kDBufs = 2;
+constexpr int kWindow = 4, kWindows = 4;     // stages per window of codes and scales, windows in the ring
 constexpr int kDqGroups = 3, kEpiGroups = 2;
 constexpr int kDqWarp0 = 4, kEpiWarp0 = kDqWarp0 + 4 * kDqGroups;
 constexpr int kThreads = 32 * (kEpiWarp0 + 4 * kEpiGroups);
@@ -63,10 +64,10 @@ constexpr int kMaxSplits = 8;
 
 struct TcSmem {
     uint8_t b[kStages][kBBytes];             // 1024-byte aligned
-    uint8_t codes[kCStages][kTileCodeBytes];
-    uint8_t scales[kCStages][kTileScaleBytes];
+    uint8_t codes[kWindows][kWindow * kTileCodeBytes];
+    uint8_t scales[kWindows][kWindow * kTileScaleBytes];
     uint64_t bfull[kStages], ready[kStages], done[kStages];   // token tile landed; both operands there; MMAs complete
-    uint64_t cfull[kCStages], cempty[kCStages];
+    uint64_t cfull[kWindows], cempty[kWindows];
     uint64_t dfull[kDBufs], dempty[kDBufs];
     uint64_t mma_done;
     uint32_t tmem_base;
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) { mbar_init(&sm.bfull[s], 1); mbar_init(&sm.ready[s], 4); mbar_init(&sm.done[s], 1); }
-        for (int s = 0; s < kCStages; ++s) { mbar_init(&sm.cfull[s], 1); mbar_init(&sm.cempty[s], 4); }
+        for (int s = 0; s < kWindows; ++s) { mbar_init(&sm.cfull[s], 1); mbar_init(&sm.cempty[s], 4 * kDqGroups); }
         for (int s = 0; s < kDBufs; ++s) { mbar_init(&sm.dfull[s], 1); mbar_init(&sm.dempty[s], 4 * kEpiGroups); }
         mbar_init(&sm.mma_done, 1);
         sm.abort_flag = 0;
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     if (warp == 0 || warp == 2) {
         if (lane == 0) {
             const bool tokens = warp == 0;
-            const int nst = tokens ? kStages : kCStages;
+            const int nst = tokens ? kStages : kWindows, step = tokens ? 1 : kWindow;
             uint64_t *full = tokens ? sm.bfull : sm.cfull, *empty = tokens ? sm.done : sm.cempty;
             if (tokens) grid_dep_wait();         // the weights are nobody's output; the tokens may be
             uint32_t issued = 0, ph = 0;
@@ -296,17 +297,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             bool ok = true;
             for (int i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
                 const Item it(a, i);
-                for (int kt = it.k0; kt < it.k1; ++kt) {
+                for (int kt = it.k0; kt < it.k1; kt += step) {
                     ok = wait_or_abort(sm, &empty[s], ph ^ 1u, err);
                     if (!ok) break;
                     if (tokens) {
                         mbar_arrive_expect_tx(&full[s], (uint32_t)a.N * 128u);
                         tma_load_2d(sm.b[s], &xmap, kt * kTileK, it.t0, &full[s]);
                     } else {
+                        // a row tile's stages follow one another in both arrays
                         const size_t tile = (size_t)it.rt * a.KT + kt;
-                        mbar_arrive_expect_tx(&full[s], kTileCodeBytes + kTileScaleBytes);
-                        bulk_g2s(sm.codes[s], a.codes + tile * kTileCodeBytes, kTileCodeBytes, &full[s]);
-                        bulk_g2s(sm.scales[s], a.scales + tile * kTileScaleBytes, kTileScaleBytes, &full[s]);
+                        const uint32_t n = (uint32_t)min(kWindow, it.k1 - kt);
+                        mbar_arrive_expect_tx(&full[s], n * (kTileCodeBytes + kTileScaleBytes));
+                        bulk_g2s(sm.codes[s], a.codes + tile * kTileCodeBytes, n * kTileCodeBytes, &full[s]);
+                        bulk_g2s(sm.scales[s], a.scales + tile * kTileScaleBytes, n * kTileScaleBytes, &full[s]);
                     }
                     ++issued;
                     if (++s == nst) { s = 0; ph ^= 1u; }
@@ -368,20 +371,28 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         const int gq = (warp - kDqWarp0) >> 2, q = (warp & 3) * 32 + lane;
         const uint32_t acol = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kACol;
         // this group's stages are the running numbers gq, gq + 3, ...; ring places are kept, not divided for
-        int sc = gq, s = gq, sa = gq, skip = gq;
-        uint32_t pc = 0, ps = 0;
+        // Every warp passes every window, those without a stage of its own too: a barrier's phase is then
+        // never two ahead of a warp that waits for it.
+        int s = gq, sa = gq, skip = gq;
+        uint32_t ps = 0, seen = 0, base = 0;     // windows passed, windows before this item
         bool ok = true;
         for (int i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
             const Item it(a, i);
             int kt = it.k0 + skip;
             for (; kt < it.k1; kt += kDqGroups) {
-                ok = wait_warp(sm, &sm.cfull[sc], pc, err);
+                const uint32_t j = (uint32_t)(kt - it.k0), win = base + j / kWindow, at = j % kWindow, w4 = win % kWindows;
+                while (seen <= win) {
+                    ok = wait_warp(sm, &sm.cfull[seen % kWindows], seen / kWindows & 1u, err);
+                    if (!ok) break;
+                    if (seen++ < win && lane == 0) mbar_arrive(&sm.cempty[(seen - 1) % kWindows]);
+                }
                 if (!ok) break;
-                const uint4 c0 = *reinterpret_cast<const uint4 *>(sm.codes[sc] + q * 16);
-                const uint4 c1 = *reinterpret_cast<const uint4 *>(sm.codes[sc] + 2048 + q * 16);
-                const uint32_t sc4 = *reinterpret_cast<const uint32_t *>(sm.scales[sc] + q * 4);
+                const uint8_t *codes = sm.codes[w4] + at * kTileCodeBytes + q * 16;
+                const uint4 c0 = *reinterpret_cast<const uint4 *>(codes), c1 = *reinterpret_cast<const uint4 *>(codes + 2048);
+                const uint32_t sc4 = *reinterpret_cast<const uint32_t *>(sm.scales[w4] + at * kTileScaleBytes + q * 4);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.cempty[sc]);
+                // the window's last stage of this group
+                if (lane == 0 && (at + kDqGroups >= kWindow || kt + kDqGroups >= it.k1)) mbar_arrive(&sm.cempty[w4]);
                 uint32_t sp[4], r[32];
                 scale_pairs(sc4 & 0xFFFFu, sp[0], sp[1]);
                 scale_pairs(sc4 >> 16, sp[2], sp[3]);
@@ -404,11 +415,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 tc_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.ready[s]);
-                if ((sc += kDqGroups) >= kCStages) { sc -= kCStages; pc ^= 1u; }
                 if ((s += kDqGroups) >= kStages) { s -= kStages; ps ^= 1u; }
                 if ((sa += kDqGroups) >= kAStages) sa -= kAStages;
             }
             skip = kt - it.k1;                   // of the next item's first stages
+            base += (uint32_t)(it.k1 - it.k0 + kWindow - 1) / kWindow;
         }
     } else if (warp >= kEpiWarp0) {
         const int eg = (warp - kEpiWarp0) >> 2, q = (warp & 3) * 32 + lane;
