@@ -360,8 +360,10 @@ TFMOE_API tfmoe_status tfmoe_route_noalloc(const uint16_t *x, int32_t T, int32_t
  *
  * The products are exact (an E2M1 value times an E4M3 value has at most 6 significant bits,
  * a bf16 value 8), the sums, bias, activation and residual are fp32, and the result is
- * rounded once. Two regimes, chosen by T (see tfmoe_linear_desc.flags to force one): a
- * weight-streaming kernel for decode-sized batches and a tcgen05 kernel above.
+ * rounded once. Two regimes (see tfmoe_linear_desc.flags to force one): a weight-streaming
+ * kernel for up to 16 tokens over large matrices, and a tcgen05 kernel for more tokens and
+ * for small matrices. Equal calls give equal bits; results of different T may differ in the
+ * last bits of the fp32 sum.
  */
 typedef struct tfmoe_linear tfmoe_linear;   /* opaque */
 

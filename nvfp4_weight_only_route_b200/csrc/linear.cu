@@ -241,9 +241,9 @@ tfmoe_status tfmoe_linear_forward(tfmoe_linear *lin, const uint16_t *x, int64_t 
     ep.out_fp32 = f32;
     int n = 0;
     const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-    const cudaError_t e = linear_stream_fits(L, T) && !(L.desc.flags & TFMOE_FLAG_FORCE_MMA)
-                              ? launch_linear_stream(L, x, ldx, T, ep, s, &n)
-                              : launch_linear_tc(L, x, ldx, T, ep, s, &n);
+    bool stream = linear_stream_fits(L, T) && !(L.desc.flags & TFMOE_FLAG_FORCE_MMA);
+    if (stream && !(L.desc.flags & TFMOE_FLAG_FORCE_GEMV)) stream = linear_stream_clocks(L, T) <= linear_tc_clocks(L, T);
+    const cudaError_t e = stream ? launch_linear_stream(L, x, ldx, T, ep, s, &n) : launch_linear_tc(L, x, ldx, T, ep, s, &n);
     L.last_launches = n;
     if (e != cudaSuccess) return cuda_fail(e, who);
     return record_ok();

@@ -44,6 +44,8 @@ inline bool linear_gated(const Linear &L) { return L.desc.activation == TFMOE_AC
 
 cudaError_t launch_linear_repack(const Linear &L, const tfmoe_linear_weights &w, cudaStream_t s);
 bool linear_stream_fits(const Linear &L, int T);
+// Estimated times in clocks, for the choice between the two where both can.
+double linear_stream_clocks(const Linear &L, int T), linear_tc_clocks(const Linear &L, int T);
 cudaError_t linear_stream_setup(const Linear &L);
 size_t linear_stream_partial_floats(const Linear &L);
 cudaError_t launch_linear_stream(Linear &L, const uint16_t *x, int64_t ldx, int T, const LinearEpilogue &ep,

@@ -224,6 +224,15 @@ int slots_for(int T, int KT) {
 // flight for HBM) in shared memory.
 bool linear_stream_fits(const Linear &L, int T) { return T <= kMaxTokens && slots_for(T, L.KT) >= 4; }
 
+// The estimated time of a call in clocks of an SM, to set beside the tcgen05 regime's: a start (token rows,
+// first weights, joined tiles) that grows with the rows, and the SM's windows of the weight stream. Fitted to
+// launches of 1 to 16 tokens over 12 matrices. With few windows and many rows tcgen05 wins (16 x 4096 x 2 x 2688:
+// 10.9 us against 15.6), with many windows this regime (8 x 4096 x 32001: 23.0 us against 33.3).
+double linear_stream_clocks(const Linear &L, int T) {
+    const double windows = (double)L.RT * L.KT / L.num_sms / kWindow;
+    return T <= 8 ? 13000.0 + 520.0 * (T - 1) + 910.0 * windows : 21500.0 + 190.0 * (T - 9) + 1310.0 * windows;
+}
+
 cudaError_t linear_stream_setup(const Linear &)
 {
     cudaError_t e = cudaFuncSetAttribute(linear_stream_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);

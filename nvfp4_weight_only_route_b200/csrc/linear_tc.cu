@@ -21,10 +21,12 @@
 // epilogue takes into 112 registers a thread at once was as fast at 7234 tokens, but its 50 KB of
 // straight-line code came from memory in every launch: 28 us against 16 at 601 tokens.)
 //
-// Measured: 7234 x 4096 x 2 x 2688 with SwiGLU 248 us (1.29 PFLOP/s, 0.78 of the measured bf16 rate); the
-// tensor pipe works in 61 % of the cycles. The decode and the epilogue take most of the rest: with the
-// decode's arithmetic left out 212 us, without the epilogue's as well 203. 601 x 2688 x 1001 16.4 us,
-// 100 x 1536 x 4096 10.8.
+// Measured: 7234 x 4096 x 2 x 2688 with SwiGLU 221 us from rest (1.44 PFLOP/s, 0.87 of the measured bf16 burst),
+// 229 to 235 us in a row, where the power limit holds the clock (1.37, 0.98 of the measured sustained rate).
+// 601 x 2688 x 1001 13.4 us, 100 x 1536 x 4096 9.7, 16 x 4096 x 2 x 2688 10.9. Copying codes and scales stage by
+// stage kept the copying thread busier than the MMAs (250 us). Two CTAs per tile (cta_group::2, half the token
+// bytes for each) gave 213 us from rest and 221 in a row and nothing at fewer tokens: not worth a second set
+// of kernels.
 //
 // The decode: a stage must be decoded in the time of its MMAs (2 N clocks, 384 at N = 192). A conversion
 // to f16 and on to bf16 would take about 410 clocks per stage of an SM's conversion rate (36 lanes per clock
@@ -37,7 +39,8 @@
 // where they belong in one instruction, which the integer multiplier does beside the logic unit.
 //
 // Few tiles leave SMs idle, so their reductions are split: CTA (tile, split) leaves its sums in global memory,
-// and the CTA that arrives last at the tile's counter adds them in split order and finishes the tile.
+// and the CTA that arrives last at the tile's counter adds them in split order and finishes the tile, with
+// the decode warps' help (601 tokens: 16.3 us by the epilogue warps alone).
 // No CTA waits for another; equal calls give equal bits.
 #include <cuda.h>
 
@@ -55,7 +58,7 @@ constexpr int kWindow = 4, kWindows = 4;     // stages per window of codes and s
 constexpr int kDqGroups = 3, kEpiGroups = 2;
 constexpr int kDqWarp0 = 4, kEpiWarp0 = kDqWarp0 + 4 * kDqGroups;
 constexpr int kThreads = 32 * (kEpiWarp0 + 4 * kEpiGroups);
-constexpr int kEpiThreads = 128 * kEpiGroups;
+constexpr int kJoinGroups = kDqGroups + kEpiGroups, kJoinThreads = 128 * kJoinGroups;
 constexpr uint32_t kACol = kDBufs * kMaxN, kTmemCols = 512;
 static_assert(kACol + kAStages * 32 <= kTmemCols, "tensor memory");
 static_assert(kAStages < kStages, "an A slot's last use is told by the barrier of its stage");
@@ -150,7 +153,7 @@ __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::befor
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
+__device__ __forceinline__ void join_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kJoinThreads) : "memory"); }
 
 // The block scales of two E4M3 bytes times 2^112, each in both halves of a bf16x2.
 __device__ __forceinline__ void scale_pairs(uint32_t two, uint32_t &lo, uint32_t &hi) {
@@ -197,7 +200,7 @@ __device__ __forceinline__ float activate_fast(float y, int act) {
 }
 
 // One epilogue thread's place: its output column and where its next step's tokens lie.
-template <int Act, bool Fast>
+template <int Act, bool Fast, int Groups>
 struct Finisher {
     static constexpr bool kGated = Act == TFMOE_ACT_SWIGLU;
     static constexpr int kTok = kGated ? 8 : 16;   // tokens of a step that this lane finishes
@@ -220,7 +223,7 @@ struct Finisher {
         res = ep.residual ? ep.residual + (int64_t)t * ep.ldr + n : nullptr;
         out = static_cast<char *>(ep.out) + ((int64_t)t * ep.ldo + n) * (Fast ? 2 : 4);
     }
-    // A step's 16 sums of this lane's weight row; the next step is 16 kEpiGroups tokens on. The residual is
+    // A step's 16 sums of this lane's weight row; the next step is 16 Groups tokens on. The residual is
     // loaded for eight tokens before any of them is stored: out may be the residual, so the compiler moves no
     // load ahead of a store, and one load at a time would cost its latency per token.
     __device__ __forceinline__ void step(const uint32_t (&s)[16]) {
@@ -252,7 +255,7 @@ struct Finisher {
                     else *reinterpret_cast<float *>(p) = v;
                 }
             }
-            const int ahead = h + 8 < kTok ? 8 : 16 * kEpiGroups + 8 - kTok;
+            const int ahead = h + 8 < kTok ? 8 : 16 * Groups + 8 - kTok;
             if (res) res += ahead * ep.ldr;
             out += ahead * ob;
             t += ahead;
@@ -430,10 +433,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         for (int i = blockIdx.x; i < a.items; i += gridDim.x, ++n_item) {
             const Item it(a, i);
             const int steps = (min(a.N, a.T - it.t0) + 15) >> 4;
-            // after an abort a split item's warps still meet at the barriers below, and read nothing
             const int buf = (int)(n_item % kDBufs);
             const bool ok = wait_warp(sm, &sm.dfull[buf], (n_item / kDBufs) & 1u, err);
-            if (!ok && a.splits == 1) break;
+            if (!ok) break;
             tc_after();
             const uint32_t dcol = d + (uint32_t)buf * kMaxN;
             auto load = [&](int st, uint32_t (&r)[16]) {
@@ -445,49 +447,65 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                     if (lane == 0) mbar_arrive(&sm.dempty[buf]);
                 }
             };
-            if (ok && eg >= steps && lane == 0) mbar_arrive(&sm.dempty[buf]);
+            if (eg >= steps && lane == 0) mbar_arrive(&sm.dempty[buf]);
             if (a.splits > 1) {
                 float *mine = a.partial + ((size_t)i * a.N + 16 * eg) * kM + q;
 #pragma unroll 1
-                for (int st = ok ? eg : steps; st < steps; st += kEpiGroups) {
+                for (int st = eg; st < steps; st += kEpiGroups) {
                     uint32_t r[16];
                     load(st, r);
 #pragma unroll
                     for (int c = 0; c < 16; ++c) mine[c * kM] = __uint_as_float(r[c]);
                     mine += 16 * kEpiGroups * kM;
                 }
-                epilogue_sync();
-                if (threadIdx.x == kEpiWarp0 * 32) {
-                    __threadfence();             // the CTA's sums, ordered by the barrier
-                    const int last = atomicAdd(a.tickets + it.tile, 1) == a.splits - 1;
-                    if (last) a.tickets[it.tile] = 0;
-                    __threadfence();
-                    sm.is_last = last;
-                }
-                epilogue_sync();
-                const bool last = sm.is_last;
-                epilogue_sync();                 // is_last is free again
-                if (!last) continue;
+                continue;
             }
-            Finisher<Act, Fast> fin(a.ep, a.T, it.rt, q, it.t0 + 16 * eg, g0, g1);
-            const float *src = a.partial + ((size_t)it.tile * a.splits * a.N + 16 * eg) * kM + q;
+            Finisher<Act, Fast, kEpiGroups> fin(a.ep, a.T, it.rt, q, it.t0 + 16 * eg, g0, g1);
 #pragma unroll 1
             for (int st = eg; st < steps; st += kEpiGroups) {
                 uint32_t r[16];
-                if (a.splits == 1) {
-                    load(st, r);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) r[c] = __float_as_uint(__ldcg(src + c * kM));
+                load(st, r);
+                fin.step(r);
+            }
+        }
+    }
+    // A split item is its CTA's only one (the grid is one wave): the decode and epilogue warps, all free by
+    // now, join the tile in the CTA that arrives last. (After an abort they still meet here.)
+    if (a.splits > 1 && warp >= kDqWarp0) {
+        const Item it(a, (int)blockIdx.x);
+        join_sync();
+        if (threadIdx.x == kDqWarp0 * 32) {
+            __threadfence();                     // the CTA's sums, ordered by the barrier
+            const int last = atomicAdd(a.tickets + it.tile, 1) == a.splits - 1;
+            if (last) a.tickets[it.tile] = 0;
+            __threadfence();
+            sm.is_last = last;
+        }
+        join_sync();
+        if (sm.is_last) {
+            grid_dep_wait();                     // the residual may be the kernel before's
+            const int jg = (warp - kDqWarp0) >> 2, q = (warp & 3) * 32 + lane, steps = (min(a.N, a.T - it.t0) + 15) >> 4;
+            const float g0 = __ldg(a.ep.global0) * 0x1p14f, g1 = Act == TFMOE_ACT_SWIGLU ? __ldg(a.ep.global1) * 0x1p14f : 0.f;
+            Finisher<Act, Fast, kJoinGroups> fin(a.ep, a.T, it.rt, q, it.t0 + 16 * jg, g0, g1);
+            const float *src = a.partial + ((size_t)it.tile * a.splits * a.N + 16 * jg) * kM + q;
+            const size_t next = (size_t)a.N * kM;    // from a split's sums to the next's
 #pragma unroll 1
-                    for (int sp = 1; sp < a.splits; ++sp) {
-                        float u[16];
+            for (int st = jg; st < steps; st += kJoinGroups, src += 16 * kJoinGroups * kM) {
+                // two splits' sums in flight at a time; added in split order
+                uint32_t r[16];
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) u[c] = __ldcg(src + ((size_t)sp * a.N + c) * kM);
+                for (int c = 0; c < 16; ++c) r[c] = 0u;
+#pragma unroll 1
+                for (int sp = 0; sp < a.splits; sp += 2) {
+                    const float *p = src + sp * next, *p1 = sp + 1 < a.splits ? p + next : p;
+                    float u[2][16];
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) + u[c]);
+                    for (int c = 0; c < 16; ++c) { u[0][c] = __ldcg(p + c * kM); u[1][c] = __ldcg(p1 + c * kM); }
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float v = __uint_as_float(r[c]) + u[0][c];
+                        r[c] = __float_as_uint(sp + 1 < a.splits ? v + u[1][c] : v);
                     }
-                    src += 16 * kEpiGroups * kM;
                 }
                 fin.step(r);
             }
@@ -522,23 +540,24 @@ constexpr size_t kSmemBytes = sizeof(TcSmem) + 1024;
 
 struct TcPlan {
     int N, splits;
+    double clocks;
 };
 
-// The tile width and the number of splits with the least estimated time, in clocks of an SM. A stage of 64
-// columns takes its MMAs' time or, where N is small, that of issuing them; a launch ends with its last
-// epilogue (about 30 clocks a token); splits add the sums' way to global memory and back.
+// The tile width and the number of splits with the least estimated time, in clocks of an SM, fitted to
+// launches of 1 to 7234 tokens over 40 weight matrices. A stage of 64 columns takes the round of its barriers and
+// its MMAs; a launch ends with its last epilogue (about 30 clocks a token); splits add the sums' way to
+// global memory and back.
 TcPlan make_tc_plan(const Linear &L, int T) {
-    TcPlan best{16, 1};
-    double least = 1e30;
+    TcPlan best{16, 1, 1e30};
     for (int N = 16; N <= kMaxN; N += 16) {
         const int64_t tiles = (int64_t)L.RT * ((T + N - 1) / N);
         for (int S = 1; S <= kMaxSplits && S <= L.KT; ++S) {
             if (S > 1 && tiles * S > L.num_sms) break;         // the workspace holds one wave of sums
             const int64_t waves = (tiles * S + L.num_sms - 1) / L.num_sms;
-            const double stage = std::max(2.0 * N, 400.0), stages = (double)((L.KT + S - 1) / S);
-            double t = (double)waves * (stages * stage + 600.0) + 30.0 * N + 3000.0;
-            if (S > 1) t += 3000.0 + 10.0 * N + 8.0 * N * S;
-            if (t < least) { least = t; best = {N, S}; }
+            const double stage = 420.0 + 1.1 * N, stages = (double)((L.KT + S - 1) / S);
+            double t = (double)waves * (stages * stage + 600.0) + 30.0 * N + 5200.0;
+            if (S > 1) t += 3500.0 + 10.0 * N + (300.0 + 9.0 * N) * S;
+            if (t < best.clocks) best = {N, S, t};
         }
         if (N >= T) break;
     }
@@ -551,6 +570,8 @@ cudaError_t linear_tc_setup(const Linear &L)
 {
     return cudaFuncSetAttribute(tc_kernel(L), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
 }
+
+double linear_tc_clocks(const Linear &L, int T) { return make_tc_plan(L, T).clocks; }
 
 size_t linear_tc_partial_floats(const Linear &L) {
     return (size_t)L.num_sms * std::min(kMaxN, (L.desc.max_tokens + 15) & ~15) * kM;
