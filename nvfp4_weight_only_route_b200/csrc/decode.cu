@@ -15,8 +15,8 @@
 //   barrier 1  (the ring fills with down tiles meanwhile)
 //   down       per expert of the run: a = silu(G) U from the pieces, as operand rows; sums -> global
 //   barrier 2
-//   combine    out = bf16(sum_s g_s y_s + residual), slots in order; with norm weights one CTA per
-//              token, which then has the row for its RMS norm
+//   combine    out = bf16(sum_s g_s y_s + residual), slots in order, the tiles of 128 outputs spread over
+//              the SMs; with norm weights one CTA per token, which then has the row for its RMS norm
 //
 // The down run's first tiles are on chip before barrier 1 opens, so HBM idles only where a ring's
 // worth of bytes (about 180 KB per SM, 4 us) does not cover a barrier. All sums across CTAs are added
@@ -62,6 +62,7 @@ struct DecodeArgs {
     uint16_t *out, *out_norm;
     double eps;
     int slots, debug;
+    uint32_t row_area;
     uint32_t test_wait_ns;
     int32_t *err_word;
 };
@@ -130,17 +131,19 @@ __device__ __forceinline__ double shifted_double_hi(uint32_t u) {
     return __hiloint2double((int)(((uint32_t)((int)u >> 3)) & 0x8FFFE000u), 0);
 }
 
-// Logits of the CTA's experts for every token: each token's columns are split over `wpt` warps.
+// Logits of the CTA's experts for every token: the columns of each (expert, token) are split over `wpt` warps.
 __device__ void router_logits(const DecodeArgs &a, double *part) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chunks = a.H / 8, G = (int)gridDim.x;
+    const int pairs = (a.E - (int)blockIdx.x + G - 1) / G * a.T;     // none for a CTA past the experts
     int wpt = kConsumers;
-    while (wpt * a.T > kConsumers) wpt >>= 1;
-    const int t = warp / wpt, p = warp % wpt, chunks = a.H / 8;
-    const uint4 *xrow = reinterpret_cast<const uint4 *>(a.x + (size_t)t * a.H);
-    for (int e = blockIdx.x; e < a.E; e += gridDim.x) {
+    while (wpt > 1 && wpt * pairs > kConsumers) wpt >>= 1;
+    const int p = warp % wpt;
+    for (int first = 0; first < pairs; first += kConsumers / wpt) {
+        const int pair = first + warp / wpt, t = pair % a.T, e = (int)blockIdx.x + pair / a.T * G;
+        const uint4 *xrow = reinterpret_cast<const uint4 *>(a.x + (size_t)t * a.H);
         const uint4 *wrow = reinterpret_cast<const uint4 *>(a.router_w + (size_t)e * a.H);
         double acc = 0.0;
-        if (t < a.T) {
+        if (pair < pairs) {
             for (int i0 = p * 32 + lane; i0 < chunks; i0 += 4 * 32 * wpt) {
                 uint4 wv[4], xv[4];
 #pragma unroll
@@ -164,13 +167,15 @@ __device__ void router_logits(const DecodeArgs &a, double *part) {
             if (lane == 0) part[warp] = acc;
         }
         consumer_sync();
-        if (threadIdx.x < a.T) {
+        const int mine = first + (int)threadIdx.x;
+        if ((int)threadIdx.x < kConsumers / wpt && mine < pairs) {
+            const int te = mine % a.T, ee = (int)blockIdx.x + mine / a.T * G;
             double v = 0.0;
             for (int i = 0; i < wpt; ++i) v += part[threadIdx.x * wpt + i];
             float l = (float)(v * 0x1p896);
-            if (a.bias) l = l + __ldg(a.bias + e);
+            if (a.bias) l = l + __ldg(a.bias + ee);
             if (a.debug && !isfinite(l)) atomicOr(a.err_word, DEV_ERR_NONFINITE);
-            a.logits[(size_t)threadIdx.x * a.E + e] = l;
+            a.logits[(size_t)te * a.E + ee] = l;
         }
         consumer_sync();
     }
@@ -243,32 +248,45 @@ __device__ void make_plan(const DecodeArgs &a, Plan &pl) {
     consumer_sync();
 }
 
-// a = silu(G) U of the plan's rows [ra, rb) as operand rows 0, 1, ..., from the gate/up pieces.
+// a = silu(G) U of the plan's rows [ra, rb) as operand rows 0, 1, ..., from the gate/up pieces. A thread holds
+// the values of its first kHold items between finding the row's largest and writing; the rest is computed again.
+// Two items' loads are in flight at a time: with one, 8 rows of 768 took 7 us of latency, with four, the code
+// of one token's few items cost it 1 us.
+template <int kHold>
 __device__ void prepare_a(const DecodeArgs &a, const Plan &pl, int ra, int rb, const Runs &r1, uint8_t *rows, uint32_t *emax) {
     const int RT = a.I / 64, KT = a.H / kTileK, KT2 = a.I / kTileK, half = a.I / 2;
     const size_t stride = (size_t)a.T * 32;              // from a tile's piece to its next, in float4
     // an item is two neighbouring outputs of one row; a warp's 32 items share the row and the row tile
-    auto value = [&](int item) {
+    struct Place { const float4 *p; uint32_t n; float g0, g1; };
+    auto place = [&](int item) {
         const int r = item / half, jp = item - r * half, rt = jp >> 5, ei = pl.ei[ra + r], e = pl.list[ei];
-        const float g0 = __ldg(a.gate_global + e), g1 = __ldg(a.up_global + e);
-        const uint32_t q = (uint32_t)(ei * RT + rt) * (uint32_t)KT, ca = r1.owner(q), n = r1.owner(q + KT - 1) - ca + 1;
-        const float4 *p = reinterpret_cast<const float4 *>(a.gu_part + piece_at(pl.poff[ei], RT, rt, pl.cnt[ei], ca, a.T) +
-                                                           (ra + r - pl.poff[ei]) * 128) + (jp & 31);
-        float4 v[4], s = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](const float4 &u) { s.x += u.x; s.y += u.y; s.z += u.z; s.w += u.w; };
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i == 0 || i < (int)n) v[i] = __ldcg(p + i * stride);
-        s = v[0];
-#pragma unroll
-        for (int i = 1; i < 4; ++i)
-            if (i < (int)n) add(v[i]);
-        for (uint32_t i = 4; i < n; ++i) add(__ldcg(p + i * stride));
-        return make_float2(silu_f32(s.x * g0) * (s.y * g1), silu_f32(s.z * g0) * (s.w * g1));
+        const uint32_t q = (uint32_t)(ei * RT + rt) * (uint32_t)KT, ca = r1.owner(q);
+        return Place{reinterpret_cast<const float4 *>(a.gu_part + piece_at(pl.poff[ei], RT, rt, pl.cnt[ei], ca, a.T) +
+                                                      (ra + r - pl.poff[ei]) * 128) + (jp & 31),
+                     r1.owner(q + KT - 1) - ca + 1, __ldg(a.gate_global + e), __ldg(a.up_global + e)};
     };
-    constexpr int kHold = 3;
-    float2 hold[kHold];
+    // The values of kBatch items, their loads in flight together; an item past the last is the last once more.
+    constexpr int kBatch = 2;
     const int items = (rb - ra) * half;
+    auto values = [&](int item, float2 *out) {
+        Place w[kBatch];
+        float4 v[kBatch], u[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            w[j] = place(min(item + j * kConsumerThreads, items - 1));
+            v[j] = __ldcg(w[j].p);
+            u[j] = __ldcg(w[j].n > 1 ? w[j].p + stride : w[j].p);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            float4 s = v[j];
+            auto add = [&](const float4 &o) { s.x += o.x; s.y += o.y; s.z += o.z; s.w += o.w; };
+            if (w[j].n > 1) add(u[j]);
+            for (uint32_t i = 2; i < w[j].n; ++i) add(__ldcg(w[j].p + i * stride));
+            out[j] = make_float2(silu_f32(s.x * w[j].g0) * (s.y * w[j].g1), silu_f32(s.z * w[j].g0) * (s.w * w[j].g1));
+        }
+    };
+    float2 hold[kHold];
     auto note = [&](int item, float2 v) {
         const uint32_t bits = max(__float_as_uint(v.x) & 0x7FFFFFFFu, __float_as_uint(v.y) & 0x7FFFFFFFu);
         const uint32_t b = __reduce_max_sync(0xffffffffu, bits >> 23);
@@ -276,17 +294,18 @@ __device__ void prepare_a(const DecodeArgs &a, const Plan &pl, int ra, int rb, c
     };
     for (int i = threadIdx.x; i < rb - ra; i += kConsumerThreads) emax[i] = 0;
     consumer_sync();
+    // a warp's lanes have items of one row, all of them or none (half is a multiple of 32)
+    for (int j0 = 0, item = threadIdx.x; item < items; j0 += kBatch, item += kBatch * kConsumerThreads) {
+        float2 v[kBatch];
+        values(item, v);
 #pragma unroll
-    for (int j = 0; j < kHold; ++j) {
-        const int item = threadIdx.x + j * kConsumerThreads;
-        if (item < items) hold[j] = value(item);
-    }
+        for (int j = 0; j < kBatch; ++j) {
+            if (item + j * kConsumerThreads < items) note(item + j * kConsumerThreads, v[j]);
 #pragma unroll
-    for (int j = 0; j < kHold; ++j) {
-        const int item = threadIdx.x + j * kConsumerThreads;
-        if (item < items) note(item, hold[j]);
+            for (int h = 0; h < kHold; h += kBatch)
+                if (j0 == h) hold[h + j] = v[j];
+        }
     }
-    for (int item = threadIdx.x + kHold * kConsumerThreads; item < items; item += kConsumerThreads) note(item, value(item));
     consumer_sync();
     auto put = [&](int item, float2 v) {
         const int r = item / half, j = 2 * (item - r * half);
@@ -299,13 +318,20 @@ __device__ void prepare_a(const DecodeArgs &a, const Plan &pl, int ra, int rb, c
         const int item = threadIdx.x + j * kConsumerThreads;
         if (item < items) put(item, hold[j]);
     }
-    for (int item = threadIdx.x + kHold * kConsumerThreads; item < items; item += kConsumerThreads) put(item, value(item));
+    for (int item = threadIdx.x + kHold * kConsumerThreads; item < items; item += kBatch * kConsumerThreads) {
+        float2 v[kBatch];
+        values(item, v);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (item + j * kConsumerThreads < items) put(item + j * kConsumerThreads, v[j]);
+    }
     consumer_sync();
 }
 
-// The weighted sum of token t's slots (plus the residual) at h = 64 hb + 2 lane and h + 1, by one warp.
-__device__ __forceinline__ float2 combine64(const DecodeArgs &a, const Plan &pl, int t, int hb, const Runs &r2) {
-    const int lane = threadIdx.x & 31, kx = a.k + a.m, RT = a.H / kTileRows, KT = a.I / kTileK, rt = hb >> 1;
+// The weighted sum of token t's slots (plus the residual) at h = 128 rt + 4 lane and the three after it, by one
+// warp, rounded to bf16: two words.
+__device__ __forceinline__ uint2 combine128(const DecodeArgs &a, const Plan &pl, int t, int rt, const Runs &r2) {
+    const int lane = threadIdx.x & 31, kx = a.k + a.m, RT = a.H / kTileRows, KT = a.I / kTileK;
     // lane s finds the pieces of slot s
     uint32_t base = 0, n = 0;
     float w = 0.f;
@@ -316,52 +342,53 @@ __device__ __forceinline__ float2 combine64(const DecodeArgs &a, const Plan &pl,
         n = r2.owner(q + KT - 1) - ca + 1;
         w = pl.w[p];
     }
-    const uint32_t col = (uint32_t)(hb & 1) * 64u + 2u * lane, most = __reduce_max_sync(0xffffffffu, n);
-    float2 acc = make_float2(0.f, 0.f);
-    for (int s0 = 0; s0 < kx; s0 += 8) {
-        float2 v[8], u[8];
+    const size_t at = (size_t)t * a.H + rt * 128 + 4 * lane;
+    const uint2 res = a.residual ? *reinterpret_cast<const uint2 *>(a.residual + at) : make_uint2(0u, 0u);
+    const uint32_t most = __reduce_max_sync(0xffffffffu, n);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [](float4 &s, const float4 &o) { s.x += o.x; s.y += o.y; s.z += o.z; s.w += o.w; };
+    constexpr int kS = 8;                                // slots in flight, two pieces of each
+    for (int s0 = 0; s0 < kx; s0 += kS) {
+        float4 v[kS], u[kS];
+        auto load = [&](float4 (&o)[kS], uint32_t i) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t b = __shfl_sync(0xffffffffu, base, (s0 + j) & 31), c = __shfl_sync(0xffffffffu, n, (s0 + j) & 31);
-            v[j] = u[j] = make_float2(0.f, 0.f);
-            const float2 *src = reinterpret_cast<const float2 *>(a.d_part + b + col);
-            if (s0 + j < kx && c > 0) v[j] = __ldcg(src);
-            if (s0 + j < kx && c > 1) u[j] = __ldcg(src + a.T * 64);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) { v[j].x += u[j].x; v[j].y += u[j].y; }
-        for (uint32_t i = 2; i < most; ++i) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < kS; ++j) {
                 const uint32_t b = __shfl_sync(0xffffffffu, base, (s0 + j) & 31), c = __shfl_sync(0xffffffffu, n, (s0 + j) & 31);
-                u[j] = make_float2(0.f, 0.f);
-                if (s0 + j < kx && i < c) u[j] = __ldcg(reinterpret_cast<const float2 *>(a.d_part + b + i * a.T * 128u + col));
+                o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (s0 + j < kx && i < c) o[j] = __ldcg(reinterpret_cast<const float4 *>(a.d_part + b + i * a.T * 128u) + lane);
             }
+        };
+        load(v, 0);
+        for (uint32_t i = 1; i < most; ++i) {
+            load(u, i);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) { v[j].x += u[j].x; v[j].y += u[j].y; }
+            for (int j = 0; j < kS; ++j) add(v[j], u[j]);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kS; ++j) {
             const float g = __shfl_sync(0xffffffffu, w, (s0 + j) & 31);
             if (s0 + j < kx) {
                 acc.x = fmaf(g, v[j].x, acc.x);
                 acc.y = fmaf(g, v[j].y, acc.y);
+                acc.z = fmaf(g, v[j].z, acc.z);
+                acc.w = fmaf(g, v[j].w, acc.w);
             }
         }
     }
-    if (a.residual) {
-        const uint32_t r = *reinterpret_cast<const uint32_t *>(a.residual + (size_t)t * a.H + hb * 64 + 2 * lane);
-        acc.x += bf16_bits_to_float(r & 0xFFFFu);
-        acc.y += bf16_bits_to_float(r >> 16);
-    }
-    return acc;
+    if (a.residual) add(acc, make_float4(bf16_bits_to_float(res.x & 0xFFFFu), bf16_bits_to_float(res.x >> 16),
+                                         bf16_bits_to_float(res.y & 0xFFFFu), bf16_bits_to_float(res.y >> 16)));
+    const uint2 o = make_uint2((uint32_t)float_to_bf16_bits_rn(acc.x) | ((uint32_t)float_to_bf16_bits_rn(acc.y) << 16),
+                               (uint32_t)float_to_bf16_bits_rn(acc.z) | ((uint32_t)float_to_bf16_bits_rn(acc.w) << 16));
+    *reinterpret_cast<uint2 *>(a.out + at) = o;
+    return o;
 }
 
 struct Layout {
     uint32_t rows, sums, zeros, emax, bars, total;
-    __host__ __device__ Layout(int T, int KT1, int KT2, int slots) {
+    // row_area: for the T rows of x and, later, the a rows of as many experts as fit
+    __host__ __device__ Layout(int T, uint32_t row_area, int slots) {
         rows = (uint32_t)slots * kSlotBytes;
-        sums = rows + (uint32_t)T * row_bytes(KT1 > KT2 ? KT1 : KT2);
+        sums = rows + row_area;
         zeros = sums + 2u * T * kSumStride * 4;
         emax = zeros + 256;                              // of the x rows and the a rows
         bars = emax + (kMaxTokens + kMaxPairs) * 4;
@@ -376,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
     __shared__ Plan pl;
     __shared__ double part[kConsumers];
     const int KT1 = a.H / kTileK, RT1 = a.I / 64, KT2 = a.I / kTileK, RT2 = a.H / kTileRows;
-    const Layout lay(a.T, KT1, KT2, a.slots);
+    const Layout lay(a.T, a.row_area, a.slots);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + lay.bars);
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t G = gridDim.x, c = blockIdx.x;
@@ -435,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
 
     router_logits(a, part);
     grid_arrive(arrive0);
-    convert_rows<8, false>(a.x, a.H, rows, a.T, a.H, KT1, emax, [](int) { return true; });
+    convert_rows<8 * NT, false>(a.x, a.H, rows, a.T, a.H, KT1, emax, [](int) { return true; });
     grid_wait(ring, arrive0, G);
     // counter 2 still holds the last call's arrivals; everyone's next use of it is behind barrier 1
     if (c == 0 && threadIdx.x == 0) *arrive2 = 0;
@@ -459,32 +486,43 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
     const uint32_t rows_at = ring.slots + lay.rows;
     const int g = lane >> 2, t = lane & 3;
     // the a rows of as many of the down run's experts as fit are prepared together: rows [r0, r_end)
-    const int fit = (int)((uint32_t)a.T * row_bytes(KT1 > KT2 ? KT1 : KT2) / row_bytes(KT2));
+    const int fit = (int)(a.row_area / row_bytes(KT2));
     int r0 = 0, r_end = 0;
 #pragma unroll 1
     for (int down = 0; down < 2; ++down) {
-        if (down) {
-            grid_arrive(arrive1);
-            grid_wait(ring, arrive1, G);
-            if (c == 0 && threadIdx.x == 0) *arrive0 = 0;
-        }
+        if (down) grid_arrive(arrive1);
         const int RT = down ? RT2 : RT1, KT = down ? KT2 : KT1;
         const uint32_t rb = row_bytes(KT);
         const uint32_t *em = down ? emax + kMaxTokens : emax;
         Pieces p(down ? r2.first(c) : r1.first(c), down ? r2.end(c) : r1.end(c), RT, KT);
-        if (p.valid()) in.fetch();
+        // the a rows of expert ei of the run and of those after it that fit: [r0, r_end)
+        auto next_rows = [&](int ei) {
+            const int last = (int)((p.end - 1) / ((uint32_t)RT2 * KT2));
+            r0 = uniform(pl.poff[ei]);
+            int el = ei;
+            while (el < last && pl.poff[el + 1] + pl.cnt[el + 1] - r0 <= fit) ++el;
+            r_end = uniform(pl.poff[el] + pl.cnt[el]);
+        };
+        if (p.valid()) {
+            in.fetch();
+            if (down) next_rows(p.ei);
+        }
+        bool prepared = false;
+        if (down) {
+            grid_wait(ring, arrive1, G);
+            if (c == 0 && threadIdx.x == 0) *arrive0 = 0;
+        }
         while (p.valid()) {
             const int ei = p.ei, m = uniform(pl.cnt[ei]), poff = uniform(pl.poff[ei]);
             float scale = 1.f;
             if (down) {
-                if (poff >= r_end) {
-                    const int last = (int)((p.end - 1) / ((uint32_t)RT2 * KT2));
-                    int el = ei;
-                    while (el < last && pl.poff[el + 1] + pl.cnt[el + 1] - poff <= fit) ++el;
-                    r0 = poff;
-                    r_end = uniform(pl.poff[el] + pl.cnt[el]);
-                    consumer_sync();                     // the rows in use are free
-                    prepare_a(a, pl, r0, r_end, r1, rows, emax + kMaxTokens);
+                if (!prepared || poff >= r_end) {
+                    if (prepared) {
+                        next_rows(ei);
+                        consumer_sync();                 // the rows in use are free
+                    }
+                    prepare_a<NT == 1 ? 8 : 4>(a, pl, r0, r_end, r1, rows, emax + kMaxTokens);
+                    prepared = true;
                 }
                 scale = __ldg(a.down_global + pl.list[ei]);
             }
@@ -519,31 +557,25 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
         }
     }
     grid_arrive(arrive2);
-    const int blocks = a.H / 64;
-    if (a.norm_w ? (int)c >= a.T : (int)c * kConsumers >= a.T * blocks) return;
+    if ((int)c >= (a.norm_w ? a.T : a.T * RT2)) return;
     grid_wait(ring, arrive2, G);
     if (c == 0 && threadIdx.x == 0) *arrive1 = 0;
     if (!a.norm_w) {
-        for (int i = (int)c * kConsumers + warp; i < a.T * blocks; i += (int)G * kConsumers) {
-            const int t = i / blocks, hb = i - t * blocks;
-            const float2 v = combine64(a, pl, t, hb, r2);
-            *reinterpret_cast<uint32_t *>(a.out + (size_t)t * a.H + hb * 64 + 2 * lane) =
-                (uint32_t)float_to_bf16_bits_rn(v.x) | ((uint32_t)float_to_bf16_bits_rn(v.y) << 16);
-        }
+        // a few tiles for every SM rather than all of them for a few
+        for (int i = (int)c + warp * (int)G; i < a.T * RT2; i += (int)G * kConsumers) combine128(a, pl, i / RT2, i % RT2, r2);
         return;
     }
     // one CTA per token: the row in shared memory, its fp64 sum of squares, the norm (as combine.cu)
     for (int t = (int)c; t < a.T; t += (int)G) {
-        uint32_t *keep = reinterpret_cast<uint32_t *>(rows);
+        uint2 *keep = reinterpret_cast<uint2 *>(rows);
         double ss = 0.0;
-        for (int hb = warp; hb < blocks; hb += kConsumers) {
-            const float2 v = combine64(a, pl, t, hb, r2);
-            const uint32_t lo = float_to_bf16_bits_rn(v.x), hi = float_to_bf16_bits_rn(v.y);
-            *reinterpret_cast<uint32_t *>(a.out + (size_t)t * a.H + hb * 64 + 2 * lane) = lo | (hi << 16);
-            keep[hb * 32 + lane] = lo | (hi << 16);
-            const double x0 = bf16_bits_to_float(lo), x1 = bf16_bits_to_float(hi);
-            ss = fma(x0, x0, ss);
-            ss = fma(x1, x1, ss);
+        for (int rt = warp; rt < RT2; rt += kConsumers) {
+            const uint2 o = combine128(a, pl, t, rt, r2);
+            keep[rt * 32 + lane] = o;
+            const float x[4] = {bf16_bits_to_float(o.x & 0xFFFFu), bf16_bits_to_float(o.x >> 16),
+                                bf16_bits_to_float(o.y & 0xFFFFu), bf16_bits_to_float(o.y >> 16)};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ss = fma((double)x[j], (double)x[j], ss);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -553,13 +585,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
 #pragma unroll
         for (int w = 0; w < kConsumers; ++w) tot += part[w];
         const double r = 1.0 / sqrt(tot / (double)a.H + a.eps);
-        for (int hb = warp; hb < blocks; hb += kConsumers) {
-            const uint32_t o = keep[hb * 32 + lane];
-            const uint32_t gm = *reinterpret_cast<const uint32_t *>(a.norm_w + hb * 64 + 2 * lane);
-            const double lo = (double)bf16_bits_to_float(o & 0xFFFFu) * r * (double)bf16_bits_to_float(gm & 0xFFFFu);
-            const double hi = (double)bf16_bits_to_float(o >> 16) * r * (double)bf16_bits_to_float(gm >> 16);
-            *reinterpret_cast<uint32_t *>(a.out_norm + (size_t)t * a.H + hb * 64 + 2 * lane) =
-                (uint32_t)double_to_bf16_bits_rn(lo) | ((uint32_t)double_to_bf16_bits_rn(hi) << 16);
+        for (int rt = warp; rt < RT2; rt += kConsumers) {
+            const uint2 o = keep[rt * 32 + lane];
+            const uint2 gm = *reinterpret_cast<const uint2 *>(a.norm_w + rt * 128 + 4 * lane);
+            const uint32_t ow[2] = {o.x, o.y}, gw[2] = {gm.x, gm.y};
+            uint32_t nw[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const double lo = (double)bf16_bits_to_float(ow[j] & 0xFFFFu) * r * (double)bf16_bits_to_float(gw[j] & 0xFFFFu);
+                const double hi = (double)bf16_bits_to_float(ow[j] >> 16) * r * (double)bf16_bits_to_float(gw[j] >> 16);
+                nw[j] = (uint32_t)double_to_bf16_bits_rn(lo) | ((uint32_t)double_to_bf16_bits_rn(hi) << 16);
+            }
+            *reinterpret_cast<uint2 *>(a.out_norm + (size_t)t * a.H + rt * 128 + 4 * lane) = make_uint2(nw[0], nw[1]);
         }
         consumer_sync();
     }
@@ -569,9 +606,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
 constexpr int kSmemLimit = 227 * 1024 - 1024 - (int)sizeof(Plan) - (int)sizeof(double) * kConsumers - 256;
 constexpr int kMinSlots = 3;     // 55 KB in flight per SM still cover the latency of HBM
 
+uint32_t least_rows(const Layer &L, int T) { return (uint32_t)T * row_bytes(std::max(L.desc.hidden, L.desc.intermediate) / kTileK); }
 int decode_slots(const Layer &L, int T) {
-    const int left = kSmemLimit - (int)Layout(T, L.desc.hidden / kTileK, L.desc.intermediate / kTileK, 0).total;
+    const int left = kSmemLimit - (int)Layout(T, least_rows(L, T), 0).total;
     return left < 0 ? 0 : std::min(kMaxSlots, left / kSlotBytes);
+}
+// What the slots leave goes to the rows: a run that crosses into another expert then prepares both at once
+// (one token, 4096 x 2688: 3 us of the CTAs that do).
+uint32_t decode_row_area(const Layer &L, int T) {
+    const uint32_t least = least_rows(L, T);
+    return least + (((uint32_t)kSmemLimit - Layout(T, least, decode_slots(L, T)).total) & ~255u);
 }
 
 int decode_workspace_tokens(const Layer &L) { return std::min(L.desc.max_tokens, kMaxTokens); }
@@ -619,13 +663,14 @@ cudaError_t launch_decode(Layer &L, const uint16_t *x, int T, const uint16_t *re
     a.residual = residual; a.norm_w = norm_w; a.out = out; a.out_norm = out_norm;
     a.eps = (double)L.desc.norm_eps;
     a.slots = decode_slots(L, T);
+    a.row_area = decode_row_area(L, T);
     a.debug = (L.desc.flags & TFMOE_FLAG_DEBUG_CHECKS) ? 1 : 0;
     a.test_wait_ns = (L.desc.flags & TFMOE_FLAG_TEST_TIMEOUT) ? kTestWaitNs : 0;
     a.err_word = L.ws.err_word;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(L.num_sms);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Layout(T, a.H / kTileK, a.I / kTileK, a.slots).total;
+    cfg.dynamicSmemBytes = Layout(T, a.row_area, a.slots).total;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;
