@@ -32,8 +32,9 @@ BUF_LOGITS, BUF_TOPK_IDS, BUF_TOPK_WEIGHTS, BUF_EXPERT_COUNTS, BUF_EXPERT_OFFSET
 EXPORTED = ["tfmoe_create", "tfmoe_load_weights", "tfmoe_forward", "tfmoe_forward_host", "tfmoe_sync_status",
             "tfmoe_destroy", "tfmoe_last_error", "tfmoe_get_buffer", "tfmoe_last_launch_count",
             "tfmoe_profile_enable", "tfmoe_profile_read", "tfmoe_route_noalloc", "tfmoe_forward_stage",
-            "tfmoe_forward_add_norm", "tfmoe_forward_decode", "tfmoe_decode_max_tokens", "tfmoe_linear_create", "tfmoe_linear_load_weights", "tfmoe_linear_forward",
-            "tfmoe_linear_sync_status", "tfmoe_linear_last_launch_count", "tfmoe_linear_destroy"]
+            "tfmoe_forward_add_norm", "tfmoe_forward_decode", "tfmoe_decode_max_tokens", "tfmoe_linear_create",
+            "tfmoe_linear_load_weights", "tfmoe_linear_forward", "tfmoe_linear_sync_status",
+            "tfmoe_linear_last_launch_count", "tfmoe_linear_destroy"]
 
 ROUTE_NOALLOC_MAX_LOGITS = 1 << 20
 
@@ -66,6 +67,9 @@ class LinearDesc(ctypes.Structure):
 class LinearWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "codes", "scales", "global", "up_codes", "up_scales", "up_global", "bias")]
+
+
+_BF16 = ("bfloat16", "int16", "uint16")   # bf16, or its raw bits
 
 
 class TfmoeError(RuntimeError):
@@ -211,12 +215,17 @@ class MoELayer:
         import torch
         if T is None:
             T = x.shape[0]
+        H = self.desc.hidden
         if out is None:
-            out = torch.empty((T, self.desc.hidden), dtype=torch.bfloat16, device=x.device)
+            out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
         if norm_w is None:
             out_norm = None
         elif out_norm is None:
-            out_norm = torch.empty((T, self.desc.hidden), dtype=torch.bfloat16, device=x.device)
+            out_norm = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        for name, t, rows in (("x", x, T), ("residual", residual, T), ("norm_w", norm_w, 1), ("out", out, T),
+                              ("out_norm", out_norm, T)):
+            if t is not None:
+                _dense(t, name, rows, H, x.device)
         if stream is None:
             stream = torch.cuda.current_stream(x.device)
         check(self.lib.tfmoe_forward_decode(self.handle, x.data_ptr(), T, _ptr(residual), _ptr(norm_w),
@@ -285,6 +294,18 @@ class MoELayer:
             pass
 
 
+def _dense(t, name: str, rows: int, width: int, device):
+    """Refuses what the library would read as something else: at least `rows` dense bf16 rows of `width`."""
+    if t.dim() == 0 or t.shape[-1] != width or t.numel() < rows * width:
+        raise ValueError(f"{name} must hold {rows} rows of {width}, got {list(t.shape)}")
+    if str(t.dtype).replace("torch.", "") not in _BF16:
+        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, got strides {t.stride()}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
 def _rows(t, name: str, width: int, dtypes, rows: Optional[int], device):
     """(pointer, row stride in elements) of a 2-D tensor whose rows are contiguous runs of `width`."""
     if t.dim() != 2 or t.shape[1] != width or (rows is not None and t.shape[0] != rows):
@@ -297,9 +318,6 @@ def _rows(t, name: str, width: int, dtypes, rows: Optional[int], device):
         raise ValueError(f"{name} must have contiguous rows, got strides {t.stride()}")
     # the stride of a single row is arbitrary and never used
     return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else (width + 7) // 8 * 8)
-
-
-_BF16 = ("bfloat16", "int16", "uint16")   # bf16, or its raw bits
 
 
 class Linear:

@@ -424,3 +424,29 @@ def test_refusals():
     lim = wide.decode_max_tokens()
     assert 1 <= lim < 16
     wide.close()
+
+
+def test_the_binding_refuses_what_the_kernel_would_misread():
+    """Strided, narrow, mistyped or misplaced tensors: an error, and nothing written."""
+    torch, _ = _mods()
+    shape, layer = _layer(512, 256, 8, 2, seed=95)
+    L = _handle(layer, shape, 8)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    x, wide = torch.zeros((4, 512), **bf), torch.zeros((4, 1024), **bf)
+    out = torch.full((4, 512), 7.0, **bf)
+    try:
+        for error, kw in ((ValueError, dict(x=wide[:, :512])), (ValueError, dict(x=wide)), (ValueError, dict(x=x, T=5)),
+                          (TypeError, dict(x=x.half())), (ValueError, dict(x=x, residual=wide[:, ::2])),
+                          (ValueError, dict(x=x, residual=x[:3].clone())), (ValueError, dict(x=x, norm_w=x[0, :256])),
+                          (TypeError, dict(x=x, norm_w=x[0].float())), (ValueError, dict(x=x, residual=torch.zeros((4, 512), dtype=torch.bfloat16)))):
+            with pytest.raises(error):
+                L.forward_decode(out=out, **kw)
+        with pytest.raises(ValueError):
+            L.forward_decode(x, out=wide[:, :512])
+        with pytest.raises(TypeError):
+            L.forward_decode(x, out=torch.zeros((4, 512), device="cuda"))
+        assert L.sync_status() == 0 and bool((out == 7.0).all()) and not wide.any()
+        L.forward_decode(x, T=2, out=out)              # the first rows of a larger batch
+        assert L.sync_status() == 0 and not out[:2].any() and bool((out[2:] == 7.0).all())
+    finally:
+        L.close()
