@@ -69,9 +69,6 @@ class LinearWeights(ctypes.Structure):
         "codes", "scales", "global", "up_codes", "up_scales", "up_global", "bias")]
 
 
-_BF16 = ("bfloat16", "int16", "uint16")   # bf16, or its raw bits
-
-
 class TfmoeError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {message}")
@@ -222,14 +219,16 @@ class MoELayer:
             out_norm = None
         elif out_norm is None:
             out_norm = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        device, dtypes = x.device, _bf16_dtypes()
         for name, t, rows in (("x", x, T), ("residual", residual, T), ("norm_w", norm_w, 1), ("out", out, T),
                               ("out_norm", out_norm, T)):
             if t is not None:
-                _dense(t, name, rows, H, x.device)
-        if stream is None:
-            stream = torch.cuda.current_stream(x.device)
-        check(self.lib.tfmoe_forward_decode(self.handle, x.data_ptr(), T, _ptr(residual), _ptr(norm_w),
-                                            out.data_ptr(), _ptr(out_norm), stream.cuda_stream))
+                _dense(t, name, rows, H, dtypes, device)
+        if not x.is_cuda:
+            raise ValueError(f"x is on {device}, expected a CUDA device")
+        check(self.lib.tfmoe_forward_decode(self.handle, x.data_ptr(), T, _ptr(residual), _ptr(norm_w), out.data_ptr(),
+                                            _ptr(out_norm),
+                                            _current_stream(device) if stream is None else stream.cuda_stream))
         return out, out_norm
 
     def forward_raw(self, x_ptr: int, T: int, out_ptr: int, stream_handle: int) -> int:
@@ -294,12 +293,24 @@ class MoELayer:
             pass
 
 
-def _dense(t, name: str, rows: int, width: int, device):
-    """Refuses what the library would read as something else: at least `rows` dense bf16 rows of `width`."""
-    if t.dim() == 0 or t.shape[-1] != width or t.numel() < rows * width:
-        raise ValueError(f"{name} must hold {rows} rows of {width}, got {list(t.shape)}")
-    if str(t.dtype).replace("torch.", "") not in _BF16:
-        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+def _bf16_dtypes():
+    import torch
+    return (torch.bfloat16, torch.int16, torch.uint16)   # bf16, or its raw bits
+
+
+def _current_stream(device) -> int:
+    """The handle of torch's current stream on a device, without the Stream object around it (2 us a call)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _dense(t, name: str, rows: int, width: int, dtypes, device):
+    """Refuses what the library would read as something else: at least `rows` dense rows of `width`."""
+    shape = t.shape
+    if not shape or shape[-1] != width or t.numel() < rows * width:
+        raise ValueError(f"{name} must hold {rows} rows of {width}, got {list(shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {dtypes[0]}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, got strides {t.stride()}")
     if t.device != device:
@@ -308,16 +319,18 @@ def _dense(t, name: str, rows: int, width: int, device):
 
 def _rows(t, name: str, width: int, dtypes, rows: Optional[int], device):
     """(pointer, row stride in elements) of a 2-D tensor whose rows are contiguous runs of `width`."""
-    if t.dim() != 2 or t.shape[1] != width or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} must be [{'T' if rows is None else rows}, {width}], got {list(t.shape)}")
-    if str(t.dtype).replace("torch.", "") not in dtypes:
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width or (rows is not None and shape[0] != rows):
+        raise ValueError(f"{name} must be [{'T' if rows is None else rows}, {width}], got {list(shape)}")
+    if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {dtypes[0]}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if width > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if one != 1 and width > 1:
         raise ValueError(f"{name} must have contiguous rows, got strides {t.stride()}")
     # the stride of a single row is arbitrary and never used
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else (width + 7) // 8 * 8)
+    return t.data_ptr(), (ld if shape[0] > 1 else (width + 7) // 8 * 8)
 
 
 class Linear:
@@ -336,9 +349,9 @@ class Linear:
         check(self.lib.tfmoe_linear_create(ctypes.byref(self.desc), ctypes.byref(h)))
         self.handle = h
         self.device = torch.device("cuda", torch.cuda.current_device())
-        fp32 = bool(self.desc.flags & FLAG_OUT_FP32)
-        self._out_dtype = torch.float32 if fp32 else torch.bfloat16
-        self._out_names = ("float32",) if fp32 else _BF16
+        self._x_dtypes = _bf16_dtypes()
+        self._out_dtypes = (torch.float32,) if self.desc.flags & FLAG_OUT_FP32 else self._x_dtypes
+        self._widths = (in_features, out_features)
 
     def load_weights(self, w: Dict[str, "object"]):
         """w: device tensors "codes", "scales", "global", with swiglu also "up_codes", "up_scales" and
@@ -349,17 +362,17 @@ class Linear:
     def forward(self, x, residual=None, out=None, stream=None):
         """x [T, in_features] bf16 (rows may be a slice of wider ones); residual and out [T, out_features]
         likewise, out may be a bf16 residual itself. Returns out."""
-        import torch
-        K, N = self.desc.in_features, self.desc.out_features
-        xp, ldx = _rows(x, "x", K, _BF16, None, self.device)
+        K, N = self._widths
+        device, dtypes = self.device, self._x_dtypes
+        xp, ldx = _rows(x, "x", K, dtypes, None, device)
         T = x.shape[0]
         if out is None:
-            out = torch.empty((T, N), dtype=self._out_dtype, device=self.device)
-        op, ldo = _rows(out, "out", N, self._out_names, T, self.device)
-        rp, ldr = (None, 0) if residual is None else _rows(residual, "residual", N, _BF16, T, self.device)
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        check(self.lib.tfmoe_linear_forward(self.handle, xp, ldx, T, rp, ldr, op, ldo, stream.cuda_stream))
+            import torch
+            out = torch.empty((T, N), dtype=self._out_dtypes[0], device=device)
+        op, ldo = _rows(out, "out", N, self._out_dtypes, T, device)
+        rp, ldr = (None, 0) if residual is None else _rows(residual, "residual", N, dtypes, T, device)
+        check(self.lib.tfmoe_linear_forward(self.handle, xp, ldx, T, rp, ldr, op, ldo,
+                                            _current_stream(device) if stream is None else stream.cuda_stream))
         return out
 
     def sync_status(self, stream=None) -> int:
