@@ -399,6 +399,7 @@ struct Layout {
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
 {
+    using In = std::conditional_t<NT == 1, WindowConsumer<NT>, PairConsumer<NT>>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Plan pl;
     __shared__ double part[kConsumers];
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
     if (warp == kConsumers) {
         if (lane < a.slots) {
             mbar_init(bars + lane, 1);
-            mbar_init(bars + kMaxSlots + lane, kConsumers);
+            mbar_init(bars + kMaxSlots + lane, In::kArrivals);
         }
         if (lane == 0) {
             mbar_init(bars + 2 * kMaxSlots, 1);
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
     if (threadIdx.x == 0) mbar_arrive_at(planned);
 
     // gate/up, then down: one loop, so that both run the same code
-    Consumer<NT> in(ring);
+    In in(ring);
     float *buf = reinterpret_cast<float *>(smem + lay.sums), *other = buf + a.T * kSumStride;   // of sums, in turn
     const int n_act = uniform(pl.n_act);
     const Runs r1 = runs_of(n_act * RT1 * KT1, G), r2 = runs_of(n_act * RT2 * KT2, G);
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
             r_end = uniform(pl.poff[el] + pl.cnt[el]);
         };
         if (p.valid()) {
-            in.fetch();
+            in.fetch(p.windows() + p.rest());
             if (down) next_rows(p.ei);
         }
         bool prepared = false;
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
             do {
                 Acc<NT> acc;
                 acc.clear();
-                in.piece(p.ka, p.kb, p.more(), xa, two, acc);
+                in.piece(p.ka, p.kb, p.rest(), xa, two, acc);
                 join_pairs<NT>(acc, buf, m, [&](int n, int j, float v) {
                     if (8 * n + 2 * t + (j & 1) < m) dst[(8 * n + (j & 1)) * 128 + 8 * (j >> 1)] = v * f[n][j & 1];
                 });
@@ -606,10 +607,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
 constexpr int kSmemLimit = 227 * 1024 - 1024 - (int)sizeof(Plan) - (int)sizeof(double) * kConsumers - 256;
 constexpr int kMinSlots = 3;     // 55 KB in flight per SM still cover the latency of HBM
 
+// Whether a call runs the kernel for one tile of 8 tokens. Its groups take alternate windows, which wants a
+// ring of at least 4 slots; where the rows leave fewer, the kernel for two tiles runs.
+bool one_tile(int T, int slots) { return T <= 8 && slots >= 4; }
+
 uint32_t least_rows(const Layer &L, int T) { return (uint32_t)T * row_bytes(std::max(L.desc.hidden, L.desc.intermediate) / kTileK); }
 int decode_slots(const Layer &L, int T) {
     const int left = kSmemLimit - (int)Layout(T, least_rows(L, T), 0).total;
-    return left < 0 ? 0 : std::min(kMaxSlots, left / kSlotBytes);
+    const int n = left < 0 ? 0 : std::min(kMaxSlots, left / kSlotBytes);
+    return one_tile(T, n) ? n & ~1 : n;                  // an even number: WindowConsumer
 }
 // What the slots leave goes to the rows: a run that crosses into another expert then prepares both at once
 // (one token, 4096 x 2688: 3 us of the CTAs that do).
@@ -677,7 +683,7 @@ cudaError_t launch_decode(Layer &L, const uint16_t *x, int T, const uint16_t *re
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, T <= 8 ? decode_kernel<1> : decode_kernel<2>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, one_tile(T, a.slots) ? decode_kernel<1> : decode_kernel<2>, a);
     *launches += 1;
     return e != cudaSuccess ? e : cudaGetLastError();
 }

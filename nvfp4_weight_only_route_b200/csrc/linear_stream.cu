@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
         if (warp > kConsumers) return;
         if (lane < a.slots) {
             mbar_init(bars + lane, 1);
-            mbar_init(bars + kMaxSlots + lane, kConsumers);
+            mbar_init(bars + kMaxSlots + lane, WindowConsumer<NT>::kArrivals);
         }
         if (lane == 0) {
             mbar_init(bars + 2 * kMaxSlots, kConsumers);
@@ -130,14 +130,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
         const int t = 8 * n + (lane >> 2);
         xa[n] = ring.slots + lay.x + (uint32_t)(t < a.T ? t : 0) * row_bytes(a.KT);
     }
-    Consumer<NT> in(ring);
+    WindowConsumer<NT> in(ring);
     Acc<NT> acc;
-    in.fetch();
+    // windows of the piece of row tile q
+    auto windows = [&](int q) {
+        const int ka = q == q0 ? k0 & ~(kWindow - 1) : 0, kb = q == q1 ? k1 : a.KT;
+        return (kb - ka + kWindow - 1) / kWindow;
+    };
+    auto rest = [&](int q) { return q == q1 ? 0 : min(2, windows(q + 1) + (q + 1 < q1 ? 1 : 0)); };
+    in.fetch(windows(q0) + rest(q0));
     const bool cut[2] = {k0 > 0 || (q0 == q1 && k1 < a.KT), q1 > q0 && k1 < a.KT};   // the first and the last piece
     for (int q = q0; q <= q1; ++q) {
         const int ka = q == q0 ? k0 : 0, kb = q == q1 ? k1 : a.KT;
         acc.clear();
-        in.piece(ka, kb, q < q1, xa, true, acc);
+        in.piece(ka, kb, rest(q), xa, true, acc);
         float *buf = sums + ((q - q0) & 1) * a.T * kSumStride;
         const int row0 = (warp & 7) * 16 + (lane >> 2), col0 = 2 * (lane & 3);
         if (kb - ka < a.KT) {
@@ -215,7 +221,7 @@ constexpr int kSmemLimit = 227 * 1024 - 1024;   // the static part and the runti
 
 int slots_for(int T, int KT) {
     const int left = kSmemLimit - (int)Layout(T, KT, 0).total;
-    return std::min(kMaxSlots, left / kSlotBytes);
+    return std::min(kMaxSlots, left / kSlotBytes) & ~1;     // an even number: WindowConsumer
 }
 
 }  // namespace
@@ -227,10 +233,10 @@ bool linear_stream_fits(const Linear &L, int T) { return T <= kMaxTokens && slot
 // The estimated time of a call in clocks of an SM, to set beside the tcgen05 regime's: a start (token rows,
 // first weights, joined tiles) that grows with the rows, and the SM's windows of the weight stream. Fitted to
 // launches of 1 to 16 tokens over 12 matrices. With few windows and many rows tcgen05 wins (16 x 4096 x 2 x 2688:
-// 10.9 us against 15.6), with many windows this regime (8 x 4096 x 32001: 23.0 us against 33.3).
+// 10.9 us against 15.6), with many windows this regime (8 x 4096 x 32001: 21.2 us against 33.3).
 double linear_stream_clocks(const Linear &L, int T) {
     const double windows = (double)L.RT * L.KT / L.num_sms / kWindow;
-    return T <= 8 ? 13000.0 + 520.0 * (T - 1) + 910.0 * windows : 21500.0 + 190.0 * (T - 9) + 1310.0 * windows;
+    return T <= 8 ? 13000.0 + 520.0 * (T - 1) + 830.0 * windows : 21500.0 + 190.0 * (T - 9) + 1250.0 * windows;
 }
 
 cudaError_t linear_stream_setup(const Linear &)

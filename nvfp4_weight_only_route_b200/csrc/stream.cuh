@@ -11,8 +11,8 @@
 // One producer lane fills a ring of slots with bulk copies; a slot holds the units of a piece whose
 // column tiles lie in one aligned window of four (two copies: a bulk copy costs the issuing
 // lane about 100 clocks, so small ones would set the pace). 16 consumer warps: warp w takes 16 rows
-// (w mod 8) of pair w / 8 of every window's units; the two warps of a row group add their sums at the
-// end of a piece. (Two groups of 8 warps that take whole pieces in turn need no joining, but leave 8
+// (w mod 8), and the two groups of 8 share the windows (the consumers' classes below); the two warps of a row group add
+// their sums at the end of a piece. (Two groups that take whole pieces in turn need no joining, but leave 8
 // warps to keep up with HBM: the 14-token wide layer took 216 us instead of 188.)
 // The product runs on mma.sync m16n8k16 (f16 in, fp32 sums), rows of weights against up to 8 tokens
 // per instruction: the tensor core is idle most of the time either way, and this form needs no
@@ -27,6 +27,8 @@
 // The chunks of a step form the k indices of two instructions. Token operands are stored in that
 // order too: [128 columns][step 0..3][half 0..3][8 values].
 #pragma once
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -207,40 +209,171 @@ struct Acc {
 
 // What a consumer lane needs of its place, computed once.
 struct Lane {
-    uint32_t code[4];      // offsets of the lane's four words of row g inside a window's pair, step by step
+    uint32_t code[4];      // offsets of the lane's four words of row g inside a window's pair `pair`, step by step
     uint32_t scale;        // offset of row g's two scale bytes
     uint32_t sel;          // prmt selector: (scale of steps 0 and 1, of steps 2 and 3)
     uint32_t x;            // offset inside a window's columns of a token row
     int unit;              // the lane's unit of a window
     bool first;            // lane 0
-    __device__ __forceinline__ Lane() {
+    __device__ __forceinline__ explicit Lane(int pair) {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         const int row = (warp & 7) * 16 + g;
-        unit = 2 * (warp >> 3) + (t >> 1);
+        unit = 2 * pair + (t >> 1);
         first = lane == 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             code[i] = (uint32_t)(unit * kTileCodeBytes + (t & 1) * (kTileCodeBytes / 2) + row * 16 + (i ^ t) * 4);
         scale = (uint32_t)(kScaleAt + unit * kTileScaleBytes + row * 4 + (t & 1) * 2);
         sel = (t >> 1) ? 0x1032u : 0x3210u;                  // steps 0 and 1 are in 16-column block t / 2
-        x = (uint32_t)(warp >> 3) * 256u + (uint32_t)t * 16u;
+        x = (uint32_t)pair * 256u + (uint32_t)t * 16u;
         // kept in registers, not worked out anew in every window
         asm volatile("" : "+r"(code[0]), "+r"(code[1]), "+r"(code[2]), "+r"(code[3]), "+r"(scale), "+r"(sel), "+r"(x));
     }
 };
 
-// A consumer warp's way through the windows of a run of pieces. It always holds the codes of the next
-// window: each word is replaced by the next window's as soon as it is converted, across the pieces'
-// borders too, and the slot is handed back when the last of it is read.
+// The consumers' two groups of 8 warps share the windows in one of two ways, which the two classes below are. A
+// warp always holds the codes of its next pair of units: each word is replaced by the next pair's as soon as it
+// is converted, across windows and pieces, and a slot is handed back when the last of it is read.
+//
+// WindowConsumer: a group takes both pairs of every second window: one wait, one hand-back and one set of
+// counters for two pairs (0.42 us per window and SM, HBM's pace, against 0.48 with one token row). The ring has an
+// even number of slots, so that a group's windows are all the phases of every second slot, in order: a
+// group that saw only some phases of a slot could take an older phase's parity for the one it waits for.
 template <int NT>
-struct Consumer {
+struct WindowConsumer {
+    static constexpr int kArrivals = kConsumers / 2;     // that free a slot
+    const Ring &r;
+    Lane ln;
+    uint32_t slot, bar, phase;         // the slot to read next, its full barrier, its phase
+    uint32_t slot0, end;               // the group's first slot, one past the last full barrier
+    uint32_t w0[4], w1[4], s0, s1;     // codes of rows g and g + 8, their scales
+    bool mine;                         // the next window to come is this group's
+    __device__ __forceinline__ explicit WindowConsumer(const Ring &ring)
+        : r(ring), ln(0), phase(0), end(ring.full + 8u * ring.n) {
+        const uint32_t group = (uint32_t)uniform((int)(threadIdx.x >> 8));
+        slot = slot0 = ring.slots + group * kSlotBytes;
+        bar = ring.full + 8u * group;
+        mine = group == 0;
+    }
+    template <int P>
+    __device__ __forceinline__ void load(int i) {
+        constexpr uint32_t at = (uint32_t)P * 2u * kTileCodeBytes;
+        w0[i] = lds32(slot + ln.code[i] + at);
+        w1[i] = lds32(slot + ln.code[i] + (at + 128u));
+    }
+    template <int P>
+    __device__ __forceinline__ void load_scales() {
+        constexpr uint32_t at = (uint32_t)P * 2u * kTileScaleBytes;
+        s0 = lds16(slot + ln.scale + at);
+        s1 = lds16(slot + ln.scale + (at + 32u));
+    }
+    __device__ __forceinline__ void release() {
+        __syncwarp();
+        if (ln.first) mbar_arrive_at(bar + 8u * kMaxSlots);
+        slot += 2u * kSlotBytes;
+        bar += 16u;
+        if (bar >= end) {
+            slot = slot0;
+            bar -= 8u * r.n;
+            phase ^= 1u;
+        }
+    }
+    // A run of `windows` windows begins: the group's first pair of it.
+    __device__ __forceinline__ void fetch(int windows) {
+        if (windows <= (mine ? 0 : 1)) return;
+        wait_warp(r, bar, phase);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load<0>(i);
+        load_scales<0>();
+    }
+    // Pair P of the group's units of the window in hand, with scales sa and sb, against the first N of NT tiles
+    // of tokens; x + at: the lane's operands (token 8 n + g; any valid row where there is no such token) at the
+    // pair's columns. Fetches the next pair: the window's second, or with `next` the first one of
+    // the group's next window. Products E2M1 * E4M3 are exact in f16 (at most 6 significant bits, 2^-10 to 2688).
+    template <int N, int P>
+    __device__ __forceinline__ void multiply(const uint32_t (&x)[NT], uint32_t at, uint32_t sa, uint32_t sb, bool next, Acc<NT> &acc) {
+        const uint32_t h0 = __byte_perm(e4m3x2_to_f16x2(sa), 0, ln.sel), h1 = __byte_perm(e4m3x2_to_f16x2(sb), 0, ln.sel);
+        const __half2 v0 = *reinterpret_cast<const __half2 *>(&h0), v1 = *reinterpret_cast<const __half2 *>(&h1);
+        // (without a next window the loads read the slot all the same, and nobody uses them)
+        if (P == 1 && next) wait_warp(r, bar, phase);
+        load_scales<1 - P>();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t a[4], b[4];
+            e2m1x8_to_f16x2x4(w0[i], a);
+            e2m1x8_to_f16x2x4(w1[i], b);
+            load<1 - P>(i);
+            const __half2 ma = i < 2 ? __low2half2(v0) : __high2half2(v0), mb = i < 2 ? __low2half2(v1) : __high2half2(v1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                a[j] = mul_f16x2(a[j], ma);
+                b[j] = mul_f16x2(b[j], mb);
+            }
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const uint4 xv = lds128(x[n] + at + 64u * i);
+                mma_f16(acc.c[0][n], a[0], b[0], a[1], b[1], xv.x, xv.y);
+                mma_f16(acc.c[1][n], a[2], b[2], a[3], b[3], xv.z, xv.w);
+            }
+        }
+        if (P == 0) release();
+    }
+    // One piece, the column tiles [ka, kb) of a row tile; the first pair of the group's next window is held
+    // where it has one. rest: windows of the run behind the piece, as far as 2. xa: the lane's token rows; `two`:
+    // the second tile of tokens has some.
+    __device__ __forceinline__ void piece(int ka, int kb, int rest, const uint32_t (&xa)[NT], bool two, Acc<NT> &acc) {
+        const int w0th = ka & ~(kWindow - 1), all = (kb - w0th + kWindow - 1) / kWindow;
+        int i = mine ? 0 : 1;
+        mine = mine != ((all & 1) != 0);
+        uint32_t x[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[n] = xa[n] + ln.x + (uint32_t)(w0th + i * kWindow) * 128u;
+#pragma unroll 1
+        for (; i < all; i += 2) {
+            const int w = w0th + i * kWindow;
+            const bool next = i + 2 < all + rest;
+            if (w >= ka && w + kWindow <= kb) {
+                if (NT == 1 || two) {
+                    multiply<NT, 0>(x, 0u, s0, s1, next, acc);
+                    multiply<NT, 1>(x, 256u, s0, s1, next, acc);
+                } else {
+                    multiply<1, 0>(x, 0u, s0, s1, next, acc);
+                    multiply<1, 1>(x, 256u, s0, s1, next, acc);
+                }
+            } else {
+                // a window of which the piece has only some units: a lane without a unit multiplies zeros by zero scales
+                // (zero times what an earlier window or an infinite activation left there could be a NaN)
+                auto part = [&](auto pair) {
+                    constexpr int P = decltype(pair)::value;
+                    const int u = w + 2 * P + ln.unit;
+                    const bool live = u >= ka && u < kb;
+                    uint32_t xl[NT];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) xl[n] = live ? x[n] + 256u * P : r.zeros;
+                    multiply<NT, P>(xl, 0u, live ? s0 : 0u, live ? s1 : 0u, next, acc);
+                };
+                part(std::integral_constant<int, 0>());
+                part(std::integral_constant<int, 1>());
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) x[n] += 2 * kWindow * 128u;
+        }
+    }
+};
+
+// PairConsumer: a group takes one pair of every window, and a slot is free as soon as both groups hold its codes.
+// For rings of few slots and experts of few tokens: the wide layer at 14 tokens (4 slots) takes 176 us with it and
+// 187 with the other, the matrix product 16 x 4096 x 32001 (4 slots, every column used) 30.8 and 29.4.
+template <int NT>
+struct PairConsumer {
+    static constexpr int kArrivals = kConsumers;
     const Ring &r;
     Lane ln;
     uint32_t slot, bar, phase;         // the slot to read next, its full barrier, its phase
     uint32_t end;                      // one past the last full barrier
     uint32_t w0[4], w1[4], s0, s1;     // codes of rows g and g + 8, their scales
-    __device__ __forceinline__ explicit Consumer(const Ring &ring)
-        : r(ring), slot(ring.slots), bar(ring.full), phase(0), end(ring.full + 8u * ring.n) {}
+    __device__ __forceinline__ explicit PairConsumer(const Ring &ring)
+        : r(ring), ln((int)(threadIdx.x >> 8)), slot(ring.slots), bar(ring.full), phase(0), end(ring.full + 8u * ring.n) {}
 
     __device__ __forceinline__ void release() {
         __syncwarp();
@@ -253,8 +386,8 @@ struct Consumer {
             phase ^= 1u;
         }
     }
-    // The first window of a run.
-    __device__ __forceinline__ void fetch() {
+    // A run of `windows` windows begins, at least one.
+    __device__ __forceinline__ void fetch(int) {
         wait_warp(r, bar, phase);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -299,10 +432,11 @@ struct Consumer {
         }
         if (next) release();
     }
-    // One piece, the column tiles [ka, kb) of a row tile, whose first window is held; `more`: another
+    // One piece, the column tiles [ka, kb) of a row tile, whose first window is held; with `rest` > 0 another
     // piece follows, whose first window is held afterwards. xa: the lane's token rows; `two`: the
     // second tile of tokens has some.
-    __device__ __forceinline__ void piece(int ka, int kb, bool more, const uint32_t (&xa)[NT], bool two, Acc<NT> &acc) {
+    __device__ __forceinline__ void piece(int ka, int kb, int rest, const uint32_t (&xa)[NT], bool two, Acc<NT> &acc) {
+        const bool more = rest > 0;
         uint32_t x[NT];
         int w = ka & ~(kWindow - 1);
 #pragma unroll
@@ -351,7 +485,12 @@ struct Pieces {
         kb = (int)min((uint32_t)KT, ka + (end - u));
     }
     __device__ __forceinline__ bool valid() const { return u < end; }
-    __device__ __forceinline__ bool more() const { return u + (kb - ka) < end; }
+    // Windows of the piece; windows of the run behind it, as far as 2.
+    __device__ __forceinline__ int windows() const { return (kb - (ka & ~(kWindow - 1)) + kWindow - 1) / kWindow; }
+    __device__ __forceinline__ int rest() const {
+        const int left = (int)(end - u) - (kb - ka);
+        return left == 0 ? 0 : left > min(KT, kWindow) ? 2 : 1;
+    }
     __device__ __forceinline__ void next() {
         u += kb - ka;
         if (++rt == RT) { rt = 0; ++ei; }

@@ -173,6 +173,19 @@ def test_shapes(oracle_mod, H, I, E, k, m, T):
         L.close()
 
 
+def test_long_rows_that_leave_a_short_ring(oracle_mod):
+    """Up to 8 tokens of rows so long that the ring keeps 3 slots (the kernel for two tiles), and 4."""
+    for T, H in ((8, 8704), (7, 8704), (8, 8192), (9, 8192)):
+        shape, layer = _layer(H, 64, 3, 2, seed=T + H)
+        x = synth.make_x(shape, T, T)
+        L = _handle(layer, shape, T)
+        try:
+            assert L.decode_max_tokens() == T
+            _check(oracle_mod, layer, shape, x, _run(L, x))
+        finally:
+            L.close()
+
+
 @pytest.mark.parametrize("T", range(1, 17))
 def test_every_batch_with_one_handle(oracle_mod, T):
     """A handle made for 16 tokens serves fewer."""
