@@ -339,3 +339,27 @@ def test_refusals():
         forced.forward(torch.zeros((17, K), dtype=torch.bfloat16, device="cuda"))
     assert e.value.status == tfmoe.ERR_UNSUPPORTED
     forced.close()
+
+
+@pytest.mark.parametrize("regime,T,ld", [("stream", 5, 1 << 29), ("mma", 5, 1 << 29), ("auto", 260, 1 << 23)])
+def test_row_offsets_beyond_32_bits(regime, T, ld):
+    """Rows so far apart that the last ones' element offsets pass 2^31."""
+    torch, tfmoe = _torch()
+    K, N = 96, 40
+    rng = np.random.default_rng(T)
+    w = ref.make_weights(rng, K, N, bias=True)
+    xb, rb = ref.bf16_bits(rng.standard_normal((T, K))), ref.bf16_bits(rng.standard_normal((T, N)))
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    x = torch.empty((T - 1) * ld + K, **bf).as_strided((T, K), (ld, 1))
+    out = torch.empty((T - 1) * ld + N, **bf).as_strided((T, N), (ld, 1))
+    x.copy_(_dev(xb).view(torch.bfloat16))
+    out.copy_(_dev(rb).view(torch.bfloat16))          # the residual, updated in place
+    assert (T - 1) * ld >= 1 << 31
+    lin = _make(w, K, N, T, flags=FORCE[regime])
+    try:
+        lin.forward(x, residual=out, out=out)
+        assert lin.sync_status() == 0, tfmoe.last_error()
+        want, bound = ref.linear64(xb, w, "none", rb)
+        ref.check(_values(out.contiguous()), want, bound)
+    finally:
+        lin.close()
