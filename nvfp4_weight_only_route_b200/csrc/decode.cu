@@ -22,6 +22,11 @@
 // worth of bytes (about 180 KB per SM, 4 us) does not cover a barrier. All sums across CTAs are added
 // in a fixed order: equal calls give equal bits.
 //
+// Measured, calls in a row: H 2048, I 768, E 128, top 8 with one token 20.7 us, with 8 tokens 44.6 (137 MB: 3.1
+// TB/s over all, HBM's pace within the streams), with shared expert, residual and norm 52; H 4096, I 1536, 14 tokens
+// 176 (810 MB: 4.6 TB/s); H 4096, I 2688, E 256, one token 46 (151 MB: 3.3 TB/s). What bounds the small ones is the
+// latency of the phases between the streams: about 14 us with one token, 20 with 8.
+//
 // a is rounded to f16 times a power of two per token and expert: 11 significant bits, exact
 // range within 2^-39 of the row's largest (8 times finer than bf16, at no cost: f16 is what the
 // product runs on).

@@ -7,6 +7,8 @@
 // leaves its pieces' sums in global memory (at most two pieces per CTA: its first and its last), and
 // the CTA that arrives last at the tile's counter adds them in CTA order and finishes it: no
 // CTA waits for another, so the launch needs no co-residency, and equal calls give equal bits.
+// Measured, calls in a row: 1 x 2048 x 4096 7.7 us, 8 x 4096 x 32001 with fp32 out 21.2 (75 MB: 3.5 TB/s over all); a
+// start of 7 us (one row) to 12 (16 rows), and 0.42 to 0.65 us per window of 18.4 KB and SM (HBM's pace is 0.42).
 // The launch is a programmatic dependent of the one before it: the weights, which no kernel
 // writes, start to stream before that kernel has ended.
 #include <algorithm>
