@@ -126,9 +126,9 @@ __device__ __forceinline__ void grid_wait(const Ring &r, uint32_t *counter, uint
     consumer_sync();
 }
 
-// A bf16 value as a double times 2^-896: its bits moved to the double's exponent and fraction. bf16
-// subnormals become the right double subnormals; infinities and NaN become 2^-768 times 1 to 2, which
-// the scaling back turns into an infinite logit.
+// A finite bf16 value as a double times 2^-896: its bits moved to the double's exponent and fraction. bf16
+// subnormals become the right double subnormals. (Infinities and NaN would become 2^-768 times 1 to 2, a
+// finite number: router_logits looks for them.)
 __device__ __forceinline__ double shifted_double_lo(uint32_t u) {
     return __hiloint2double((int)(((uint32_t)((int)(u << 16) >> 3)) & 0x8FFFE000u), 0);
 }
@@ -148,6 +148,7 @@ __device__ void router_logits(const DecodeArgs &a, double *part) {
         const uint4 *xrow = reinterpret_cast<const uint4 *>(a.x + (size_t)t * a.H);
         const uint4 *wrow = reinterpret_cast<const uint4 *>(a.router_w + (size_t)e * a.H);
         double acc = 0.0;
+        uint32_t top = 0;                                // largest magnitude bits of x, in both halves
         if (pair < pairs) {
             for (int i0 = p * 32 + lane; i0 < chunks; i0 += 4 * 32 * wpt) {
                 uint4 wv[4], xv[4];
@@ -159,11 +160,27 @@ __device__ void router_logits(const DecodeArgs &a, double *part) {
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
+                    top = max_bits(xv[j], top);
                     const uint32_t wu[4] = {wv[j].x, wv[j].y, wv[j].z, wv[j].w}, xu[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         acc = fma(shifted_double_lo(xu[q]), (double)bf16_bits_to_float(wu[q] & 0xFFFFu), acc);
                         acc = fma(shifted_double_hi(xu[q]), (double)bf16_bits_to_float(wu[q] >> 16), acc);
+                    }
+                }
+            }
+            if (__any_sync(0xffffffffu, max(top >> 16, top & 0xFFFFu) >= 0x7F80u)) {
+                // x holds an infinity or a NaN here: the slice once more with converted values, so that the logit is
+                // the infinity or NaN that the sum of products is (the scaling back leaves those as they are)
+                acc = 0.0;
+#pragma unroll 1
+                for (int i = p * 32 + lane; i < chunks; i += 32 * wpt) {
+                    const uint4 w4 = __ldg(wrow + i), x4 = xrow[i];
+                    const uint32_t wu[4] = {w4.x, w4.y, w4.z, w4.w}, xu[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        acc = fma((double)bf16_bits_to_float(xu[q] & 0xFFFFu), (double)bf16_bits_to_float(wu[q] & 0xFFFFu), acc);
+                        acc = fma((double)bf16_bits_to_float(xu[q] >> 16), (double)bf16_bits_to_float(wu[q] >> 16), acc);
                     }
                 }
             }
