@@ -163,12 +163,14 @@ class MoELayer:
     def __init__(self, hidden: int, intermediate: int, num_experts: int, top_k: int, max_tokens: int,
                  has_router_bias: bool = False, flags: int = 0, gemv_max_tokens: int = 0,
                  shared_intermediate: int = 0, norm_eps: float = 1e-6):
+        import torch
         self.lib = load_library()
         self.desc = LayerDesc(hidden, intermediate, num_experts, top_k, max_tokens,
                               1 if has_router_bias else 0, flags, gemv_max_tokens, shared_intermediate, norm_eps)
         h = ctypes.c_void_p()
         check(self.lib.tfmoe_create(ctypes.byref(self.desc), ctypes.byref(h)))
         self.handle = h
+        self.device = torch.device("cuda", torch.cuda.current_device())
 
     def load_weights(self, w: Dict[str, "object"]):
         """w: canonical-layout device tensors (see synth.LAYER_KEYS); router_bias may be None."""
@@ -212,20 +214,17 @@ class MoELayer:
         import torch
         if T is None:
             T = x.shape[0]
-        H = self.desc.hidden
+        H, device, dtypes = self.desc.hidden, self.device, _bf16_dtypes()
+        _dense(x, "x", T, H, dtypes, device)
         if out is None:
-            out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+            out = torch.empty((T, H), dtype=torch.bfloat16, device=device)
         if norm_w is None:
             out_norm = None
         elif out_norm is None:
-            out_norm = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-        device, dtypes = x.device, _bf16_dtypes()
-        for name, t, rows in (("x", x, T), ("residual", residual, T), ("norm_w", norm_w, 1), ("out", out, T),
-                              ("out_norm", out_norm, T)):
+            out_norm = torch.empty((T, H), dtype=torch.bfloat16, device=device)
+        for name, t, rows in (("residual", residual, T), ("norm_w", norm_w, 1), ("out", out, T), ("out_norm", out_norm, T)):
             if t is not None:
                 _dense(t, name, rows, H, dtypes, device)
-        if not x.is_cuda:
-            raise ValueError(f"x is on {device}, expected a CUDA device")
         check(self.lib.tfmoe_forward_decode(self.handle, x.data_ptr(), T, _ptr(residual), _ptr(norm_w), out.data_ptr(),
                                             _ptr(out_norm),
                                             _current_stream(device) if stream is None else stream.cuda_stream))
