@@ -245,7 +245,8 @@ class MoELayer:
         return out_host
 
     def sync_status(self, stream=None) -> int:
-        return self.lib.tfmoe_sync_status(self.handle, _stream_handle(stream))
+        """Waits for `stream` (default: the current stream of the handle's device) and returns the status code."""
+        return self.lib.tfmoe_sync_status(self.handle, _current_stream(self.device) if stream is None else stream.cuda_stream)
 
     def buffer(self, which: int):
         p, n = ctypes.c_void_p(), ctypes.c_size_t()
@@ -375,7 +376,8 @@ class Linear:
         return out
 
     def sync_status(self, stream=None) -> int:
-        return self.lib.tfmoe_linear_sync_status(self.handle, _stream_handle(stream))
+        """Waits for `stream` (default: the current stream of the handle's device) and returns the status code."""
+        return self.lib.tfmoe_linear_sync_status(self.handle, _current_stream(self.device) if stream is None else stream.cuda_stream)
 
     def last_launch_count(self) -> int:
         return int(self.lib.tfmoe_linear_last_launch_count(self.handle))

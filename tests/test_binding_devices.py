@@ -76,3 +76,15 @@ def test_forward_decode_refuses_a_host_batch():
     with pytest.raises(ValueError, match="x is on cpu"):
         L.forward_decode(torch.zeros((4, 512), dtype=torch.bfloat16), stream=STREAM)
     assert L.lib.calls == []
+
+
+@pytest.mark.parametrize("kind,call", [("MoELayer", "tfmoe_sync_status"), ("Linear", "tfmoe_linear_sync_status")])
+def test_sync_status_waits_for_the_stream_its_forward_ran_on(kind, call, monkeypatch):
+    """forward and forward_decode take the current stream of the handle's device, which need not be the current
+    device; sync_status has to wait for the same one."""
+    monkeypatch.setattr(tfmoe, "_current_stream", lambda device: 100 + device.index)
+    cls = getattr(tfmoe, kind)
+    h = cls.__new__(cls)
+    h.lib, h.handle, h.device = FakeLibrary(), None, torch.device("cuda:1")
+    assert h.sync_status() == tfmoe.OK and h.sync_status(stream=STREAM) == tfmoe.OK
+    assert [(n, a[-1]) for n, a in h.lib.calls] == [(call, 101), (call, 77)]
