@@ -317,6 +317,20 @@ def _dense(t, name: str, rows: int, width: int, dtypes, device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+def _packed(t, name: str, rows: int, width: int, dtypes, device):
+    """Refuses a weight tensor that does not hold rows x width contiguous elements on the device, as [..., width] or flat."""
+    shape = tuple(t.shape)
+    flat = rows * width
+    if t.numel() < flat or not (flat == 1 or len(shape) == 1 or (shape and shape[-1] == width)):
+        raise ValueError(f"{name} must be [{rows}, {width}], got {list(shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {dtypes[0]}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, got strides {t.stride()}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
 def _rows(t, name: str, width: int, dtypes, rows: Optional[int], device):
     """(pointer, row stride in elements) of a 2-D tensor whose rows are contiguous runs of `width`."""
     shape = t.shape
@@ -355,8 +369,22 @@ class Linear:
 
     def load_weights(self, w: Dict[str, "object"]):
         """w: device tensors "codes", "scales", "global", with swiglu also "up_codes", "up_scales" and
-        "up_global", and "bias" (layouts of tfmoe_linear_weights)."""
-        ws = LinearWeights(*[_ptr(w.get(n)) for n, _ in LinearWeights._fields_])
+        "up_global", and "bias" (layouts of tfmoe_linear_weights). What the handle does not read may be missing
+        or None."""
+        import torch
+        K, N = self._widths
+        gated = self.desc.activation == ACTIVATIONS.index("swiglu")
+        bytes_, fp32 = (torch.uint8, torch.int8), (torch.float32,)
+        scales = bytes_ + (torch.float8_e4m3fn,)
+        read = {}
+        for p in ("", "up_") if gated else ("",):
+            read.update({p + "codes": (N, K // 2, bytes_), p + "scales": (N, K // 16, scales), p + "global": (1, 1, fp32)})
+        if self.desc.has_bias:
+            read["bias"] = (1, 2 * N if gated else N, fp32)
+        for name, (rows, width, dtypes) in read.items():
+            if w.get(name) is not None:
+                _packed(w[name], name, rows, width, dtypes, self.device)
+        ws = LinearWeights(*[_ptr(w.get(n)) if n in read else None for n, _ in LinearWeights._fields_])
         check(self.lib.tfmoe_linear_load_weights(self.handle, ctypes.byref(ws)))
 
     def forward(self, x, residual=None, out=None, stream=None):

@@ -88,3 +88,66 @@ def test_sync_status_waits_for_the_stream_its_forward_ran_on(kind, call, monkeyp
     h.lib, h.handle, h.device = FakeLibrary(), None, torch.device("cuda:1")
     assert h.sync_status() == tfmoe.OK and h.sync_status(stream=STREAM) == tfmoe.OK
     assert [(n, a[-1]) for n, a in h.lib.calls] == [(call, 101), (call, 77)]
+
+
+class Strided(FakeTensor):
+    def is_contiguous(self):
+        return False
+
+    def stride(self):
+        return (1, self.shape[0])
+
+
+def _linear(activation="none", has_bias=False):
+    lin = tfmoe.Linear.__new__(tfmoe.Linear)
+    lin.lib, lin.handle, lin.device, lin._widths = FakeLibrary(), None, torch.device("cuda:0"), (64, 48)
+    lin.desc = tfmoe.LinearDesc(64, 48, 4, tfmoe.ACTIVATIONS.index(activation), int(has_bias), 0)
+    return lin
+
+
+def _weights(prefixes=("",), bias=None):
+    w = {}
+    for p in prefixes:
+        w.update({p + "codes": FakeTensor((48, 32), "cuda:0", torch.uint8), p + "scales": FakeTensor((48, 4), "cuda:0", torch.uint8),
+                  p + "global": FakeTensor((1,), "cuda:0", torch.float32)})
+    if bias:
+        w["bias"] = FakeTensor((bias,), "cuda:0", torch.float32)
+    return w
+
+
+@pytest.mark.parametrize("name,error,bad", [
+    ("codes", ValueError, Strided((48, 32), "cuda:0", torch.uint8)), ("codes", ValueError, FakeTensor((32, 48), "cuda:0", torch.uint8)),
+    ("codes", ValueError, FakeTensor((47, 32), "cuda:0", torch.uint8)), ("codes", TypeError, FakeTensor((48, 32), "cuda:0", torch.int32)),
+    ("codes", ValueError, FakeTensor((48, 32), "cpu", torch.uint8)), ("codes", ValueError, FakeTensor((48, 32), "cuda:1", torch.uint8)),
+    ("scales", TypeError, FakeTensor((48, 4), "cuda:0", torch.bfloat16)), ("scales", ValueError, FakeTensor((48, 3), "cuda:0", torch.uint8)),
+    ("scales", ValueError, FakeTensor((), "cuda:0", torch.uint8)), ("global", TypeError, FakeTensor((1,), "cuda:0", torch.float64)),
+    ("global", ValueError, FakeTensor((0,), "cuda:0", torch.float32)), ("global", ValueError, FakeTensor((1,), "cpu", torch.float32)),
+    ("bias", TypeError, FakeTensor((96,), "cuda:0", torch.bfloat16)), ("bias", ValueError, FakeTensor((48,), "cuda:0", torch.float32)),
+    ("up_codes", ValueError, FakeTensor((48, 16), "cuda:0", torch.uint8)), ("up_scales", ValueError, Strided((48, 4), "cuda:0", torch.uint8)),
+    ("up_global", ValueError, FakeTensor((1,), "cuda:1", torch.float32)),
+])
+def test_load_weights_of_the_product_refuses_what_the_repack_would_misread(name, error, bad):
+    lin = _linear("swiglu", has_bias=True)
+    w = _weights(("", "up_"), bias=96)
+    w[name] = bad
+    with pytest.raises(error, match=name):
+        lin.load_weights(w)
+    assert lin.lib.calls == []
+
+
+def test_load_weights_of_the_product_takes_what_it_reads():
+    lin = _linear("swiglu", has_bias=True)
+    lin.load_weights(_weights(("", "up_"), bias=96))
+    w = _weights()
+    w["scales"] = FakeTensor((48, 4), "cuda:0", torch.float8_e4m3fn)
+    w["codes"] = FakeTensor((48 * 32,), "cuda:0", torch.uint8)          # flat
+    w["global"] = FakeTensor((), "cuda:0", torch.float32)
+    w["bias"] = torch.zeros(3)                                          # not read by a handle without a bias
+    plain = _linear()
+    plain.load_weights(w)
+    assert [n for n, _ in lin.lib.calls + plain.lib.calls] == ["tfmoe_linear_load_weights"] * 2
+    given = plain.lib.calls[0][1][1]._obj
+    assert given.codes == 4096 and given.bias is None and given.up_codes is None
+    missing = _linear()
+    missing.load_weights({"codes": w["codes"], "scales": w["scales"]})   # the library refuses a missing pointer
+    assert getattr(missing.lib.calls[0][1][1]._obj, "global") is None
