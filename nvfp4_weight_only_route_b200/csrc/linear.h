@@ -55,13 +55,35 @@ size_t linear_tc_partial_floats(const Linear &L);
 cudaError_t launch_linear_tc(Linear &L, const uint16_t *x, int64_t ldx, int T, const LinearEpilogue &ep,
                              cudaStream_t s, int *launches);
 
-// Activations in fp32. expf, erff and the division are CUDA's own fp32 functions (a few units
-// in the last place), so an fp32 output keeps its precision.
+// GELU: y Phi(y). 1 + erf cancels for negative y (4 % off at y = -5, zero from -5.6 on), so the tail is computed
+// by itself: for v = |y|, Phi(-v) = e^{-v^2/2} t q(1 - t) with t = 1 / (1 + c v), where t q is half the scaled
+// complementary error function, smooth in t. q is a polynomial fitted by reweighted least squares over v <= 14.6
+// (below -14.5 the tail is under the smallest fp32): of degree 9 and c = 25/64 to 2^-26.9; with Fast, for outputs
+// that are rounded to bf16, of degree 5 and c = 29/64 to 2^-16.9, and with the one-instruction exponential of a
+// rounded v^2. (4096 x 2048 x 8192 with bf16 out: Fast 132 us, without it 137, CUDA's erfcf 154, the cancelling form 130.)
+template <bool Fast>
+__device__ __forceinline__ float gelu(float y) {
+    constexpr float kFine[] = {0.5f, -0.521293163f, 0.0958522633f, 0.119704634f, 0.00993833877f, -0.0561364889f,
+                               0.0359269567f, -0.0946980417f, 0.096099481f, -0.029562287f};
+    constexpr float kCoarse[] = {0.499998093f, -0.380580723f, -0.0397436433f, 0.0596017055f, 0.11025656f, -0.0689856187f};
+    constexpr int kDegree = Fast ? 5 : 9;
+    const float v = fminf(fabsf(y), 15.0f), t = rcp_approx(fmaf(v, Fast ? 0.453125f : 0.390625f, 1.0f)), s = 1.0f - t;
+    float q = Fast ? kCoarse[kDegree] : kFine[kDegree];
+#pragma unroll
+    for (int i = kDegree - 1; i >= 0; --i) q = fmaf(q, s, Fast ? kCoarse[i] : kFine[i]);
+    const float v2 = v * v;
+    float e = Fast ? __expf(-0.5f * v2) : expf(-0.5f * v2);
+    if (!Fast) e = fmaf(e, -0.5f * fmaf(v, v, -v2), e);       // what the rounding of v^2 lost
+    const float tail = q * t * e;
+    return y * (y < 0.f ? tail : 1.0f - tail);                // a NaN stays a NaN
+}
+
+// Activations in fp32. expf and the division are CUDA's own fp32 functions (a few units in the last place).
 __device__ __forceinline__ float activate(float y, int act) {
     switch (act) {
     case TFMOE_ACT_RELU: return y < 0.f ? 0.f : y;            // a NaN stays a NaN
     case TFMOE_ACT_SILU: return y / (1.0f + expf(-y));
-    case TFMOE_ACT_GELU: return 0.5f * y * (1.0f + erff(y * 0.70710678118654752f));
+    case TFMOE_ACT_GELU: return gelu<false>(y);
     case TFMOE_ACT_GELU_TANH:
         // (1 + tanh(z)) / 2 = 1 / (1 + e^-2z), z = sqrt(2/pi) (y + 0.044715 y^3)
         return y / (1.0f + expf(-1.5957691216057308f * (y + 0.044715f * y * y * y)));

@@ -191,6 +191,7 @@ struct Item {
 __device__ __forceinline__ float activate_fast(float y, int act) {
     switch (act) {
     case TFMOE_ACT_SILU: return silu_f32(y);
+    case TFMOE_ACT_GELU: return gelu<true>(y);
     case TFMOE_ACT_GELU_TANH: {
         const float z = 1.5957691216057308f * (y + 0.044715f * y * y * y);
         return y * rcp_approx(1.0f + __expf(-z));
