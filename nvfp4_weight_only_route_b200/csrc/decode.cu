@@ -418,6 +418,19 @@ struct Layout {
     }
 };
 
+// The gate/up pieces of the units [u, end) once more, from global memory without rounding x.
+__device__ __forceinline__ void exact_gate_up(const DecodeArgs &a, const Plan &pl, uint32_t u, uint32_t end) {
+    consumer_sync();                                     // the pieces' first sums are written
+    for (Pieces p(u, end, a.I / 64, a.H / kTileK); p.valid(); p.next()) {
+        const int m = pl.cnt[p.ei], poff = pl.poff[p.ei];
+        const size_t tile = ((size_t)pl.list[p.ei] * p.RT + p.rt) * p.KT;
+        float *dst = a.gu_part + piece_at(poff, p.RT, p.rt, m, blockIdx.x, a.T);
+        for (int i = threadIdx.x; i < m * 128; i += kConsumerThreads)
+            dst[i] = exact_dot<false>(a.gu_codes + tile * kTileCodeBytes, a.gu_scales + tile * kTileScaleBytes, p.ka, p.kb, i & 127,
+                                      a.x + (size_t)pl.tok[poff + (i >> 7)] * a.H, a.H);
+    }
+}
+
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
 {
@@ -452,7 +465,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
         fence_mbar_init();
     }
     if (threadIdx.x < kMaxTokens * 8) reinterpret_cast<uint32_t *>(pl.sel)[threadIdx.x] = 0;
-    if (threadIdx.x < kMaxTokens) reinterpret_cast<uint32_t *>(smem + lay.emax)[threadIdx.x] = 0;
+    if (threadIdx.x < kMaxTokens) {
+        reinterpret_cast<uint32_t *>(smem + lay.emax)[threadIdx.x] = 0;
+        reinterpret_cast<uint32_t *>(smem + lay.sums)[threadIdx.x] = 0xFFFFFFFFu;   // the rows' smallest, before there are sums
+    }
     if (threadIdx.x < 64) reinterpret_cast<uint32_t *>(smem + lay.zeros)[threadIdx.x] = 0;
     __syncthreads();
 
@@ -485,7 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
 
     router_logits(a, part);
     grid_arrive(arrive0);
-    convert_rows<8 * NT, false>(a.x, a.H, rows, a.T, a.H, KT1, emax, [](int) { return true; });
+    const bool wide = convert_rows<8 * NT, false>(a.x, a.H, rows, a.T, a.H, KT1, emax, reinterpret_cast<uint32_t *>(smem + lay.sums),
+                                                  [](int) { return true; });
     grid_wait(ring, arrive0, G);
     // counter 2 still holds the last call's arrivals; everyone's next use of it is behind barrier 1
     if (c == 0 && threadIdx.x == 0) *arrive2 = 0;
@@ -513,7 +530,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
     int r0 = 0, r_end = 0;
 #pragma unroll 1
     for (int down = 0; down < 2; ++down) {
-        if (down) grid_arrive(arrive1);
+        if (down) {
+            if (wide) exact_gate_up(a, pl, r1.first(c), r1.end(c));   // x rows that f16 cannot hold
+            grid_arrive(arrive1);
+        }
         const int RT = down ? RT2 : RT1, KT = down ? KT2 : KT1;
         const uint32_t rb = row_bytes(KT);
         const uint32_t *em = down ? emax + kMaxTokens : emax;

@@ -1,9 +1,9 @@
 // linear_stream.cu -- the streaming regime of the NVFP4 matrix product: up to 16 tokens, bound by
 // the weight bytes over HBM bandwidth (stream.cuh has the stream and the arithmetic).
 //
-// The x rows become f16 times a power of two per row and CTA (exact for every element within
-// 2^28 of the largest one the CTA uses; smaller ones are rounded to 2^-39 of the largest) and stay
-// in shared memory. A row tile that one CTA owns is finished there. One that is cut by CTA borders
+// The x rows become f16 times a power of two per row and CTA and stay in shared memory: exact as long as the
+// elements that the CTA uses of a row lie within 2^31 of one another. A CTA that finds others takes its pieces'
+// sums from exact_dot instead. A row tile that one CTA owns is finished there. One that is cut by CTA borders
 // leaves its pieces' sums in global memory (at most two pieces per CTA: its first and its last), and
 // the CTA that arrives last at the tile's counter adds them in CTA order and finishes it: no
 // CTA waits for another, so the launch needs no co-residency, and equal calls give equal bits.
@@ -54,6 +54,26 @@ __device__ __forceinline__ void finish_tile(const StreamArgs &a, int rt, const f
         if (n >= a.ep.N) continue;
         const float *s = sums + t * kSumStride + (gated ? 2 * j : j);
         store_output(a.ep, t, n, finish_output(a.ep, t, n, s[0], gated ? s[1] : 0.f, g0, g1));
+    }
+}
+
+// The CTA's pieces once more, from global memory without rounding x; the products above stored nothing.
+__device__ __forceinline__ void exact_pieces(const StreamArgs &a, int q0, int k0, int q1, int k1, float *sums, float g0, float g1) {
+    for (int q = q0; q <= q1; ++q) {
+        const int ka = q == q0 ? k0 : 0, kb = q == q1 ? k1 : a.KT;
+        const bool cut = kb - ka < a.KT;
+        float *mine = a.partial + (size_t)(2 * blockIdx.x + (q != q0)) * a.T * 128;
+        consumer_sync();                                    // the sums are free
+        for (int i = threadIdx.x; i < a.T * 128; i += kConsumerThreads) {
+            const int t = i >> 7, row = i & 127;
+            const float v = exact_dot<true>(a.codes + (size_t)q * a.KT * kTileCodeBytes, a.scales + (size_t)q * a.KT * kTileScaleBytes,
+                                            ka, kb, row, a.x + (int64_t)t * a.ldx, a.K);
+            if (cut) mine[i] = v;
+            else sums[t * kSumStride + row] = v;
+        }
+        if (cut) continue;
+        consumer_sync();
+        finish_tile(a, q, sums, g0, g1);
     }
 }
 
@@ -112,19 +132,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
     }
 
     take_registers();
-    if (threadIdx.x < kMaxTokens) emax[threadIdx.x] = 0;
+    uint32_t *low = reinterpret_cast<uint32_t *>(sums);      // before there are sums
+    if (threadIdx.x < kMaxTokens) {
+        emax[threadIdx.x] = 0;
+        low[threadIdx.x] = 0xFFFFFFFFu;
+    }
     if (threadIdx.x < 64) reinterpret_cast<uint32_t *>(smem + lay.zeros)[threadIdx.x] = 0;
     const bool gated = a.ep.act == TFMOE_ACT_SWIGLU;
     const float g0 = __ldg(a.ep.global0), g1 = gated ? __ldg(a.ep.global1) : 0.f;
     asm volatile("bar.sync 10, %0;" ::"n"(kConsumerThreads + 32) : "memory");
     grid_dep_wait();                                        // before anything another kernel may write
-    {
-        const bool all = q1 > q0 + 1;
-        convert_rows<8 * NT, true>(a.x, a.ldx, smem + lay.x, a.T, a.K, a.KT, emax, [&](int kg) {
-            const bool from = kg >= k0 / 2, to = kg <= (k1 - 1) / 2;
-            return all || (q1 == q0 ? from && to : from || to);
-        }, requested);
-    }
+    const bool all = q1 > q0 + 1;
+    const bool wide = convert_rows<8 * NT, true>(a.x, a.ldx, smem + lay.x, a.T, a.K, a.KT, emax, low, [&](int kg) {
+        const bool from = kg >= k0 / 2, to = kg <= (k1 - 1) / 2;
+        return all || (q1 == q0 ? from && to : from || to);
+    }, requested);
+    const int joined = wide ? 0 : a.T;                      // columns of sums to finish
 
     uint32_t xa[NT];
 #pragma unroll
@@ -150,12 +173,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
         const int row0 = (warp & 7) * 16 + (lane >> 2), col0 = 2 * (lane & 3);
         if (kb - ka < a.KT) {
             float *mine = a.partial + (size_t)(2 * c + (q != q0)) * a.T * 128;
-            join_pairs<NT>(acc, buf, a.T, [&](int i, int j, float v) {
+            join_pairs<NT>(acc, buf, joined, [&](int i, int j, float v) {
                 const int col = 8 * i + col0 + (j & 1), row = row0 + 8 * (j >> 1);
                 if (col < a.T) mine[col * 128 + row] = v * inverse_up(emax[col]);
             });
         } else if (gated) {
-            join_pairs<NT>(acc, buf, a.T, [&](int i, int j, float v) {
+            join_pairs<NT>(acc, buf, joined, [&](int i, int j, float v) {
                 const int col = 8 * i + col0 + (j & 1), row = row0 + 8 * (j >> 1);
                 const float other = __shfl_xor_sync(0xffffffffu, v, 4);          // the neighbouring row
                 const int n = (q * 128 + row) >> 1;
@@ -164,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
                 store_output(a.ep, col, n, finish_output(a.ep, col, n, v * inv, other * inv, g0, g1));
             });
         } else {
-            join_pairs<NT>(acc, buf, a.T, [&](int i, int j, float v) {
+            join_pairs<NT>(acc, buf, joined, [&](int i, int j, float v) {
                 const int col = 8 * i + col0 + (j & 1), row = row0 + 8 * (j >> 1);
                 const int n = q * 128 + row;
                 if (col < a.T && n < a.ep.N)
@@ -172,6 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
             });
         }
     }
+    if (wide) exact_pieces(a, q0, k0, q1, k1, sums, g0, g1);
     if (!cut[0] && !cut[1]) return;
     consumer_sync();
     if (threadIdx.x < 2) {

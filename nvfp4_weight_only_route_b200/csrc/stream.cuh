@@ -561,6 +561,24 @@ __device__ __forceinline__ uint32_t max_bits(const uint4 &v, uint32_t m) {
     for (int j = 0; j < 4; ++j) asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(u[j] & 0x7FFF7FFFu));
     return m;
 }
+// Smallest magnitude bits less one of eight bf16 values, zeros left out (they become 0xFFFF), in both halves of a word.
+__device__ __forceinline__ uint32_t min_bits(const uint4 &v, uint32_t m) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t less;
+        asm("add.u16x2 %0, %1, %2;" : "=r"(less) : "r"(u[j] & 0x7FFF7FFFu), "r"(0xFFFFFFFFu));
+        asm("min.u16x2 %0, %0, %1;" : "+r"(m) : "r"(less));
+    }
+    return m;
+}
+// Whether a row has elements that its f16 operand cannot hold: the last bit of an element, 2^(field - 134), has to be
+// at least f16's last one, 2^-24, times the row's power of two, so the fields may be 31 apart. low: min_bits of the row. A row with
+// an infinity or a NaN is not one of these: its outputs are infinite or NaN whatever its other elements are.
+__device__ __forceinline__ bool wide_row(uint32_t emax, uint32_t low) {
+    return emax < 255u && (int)emax - max((int)((low + 1) >> 7), 1) > 31;
+}
+
 // The power of two that brings a row whose largest exponent field is emax just below 2^15, as the
 // exponent field of its float; the inverse's field is 254 minus it.
 __device__ __forceinline__ int up_field(uint32_t emax) {
@@ -572,16 +590,17 @@ __device__ __forceinline__ float inverse_up(uint32_t emax) {
 }
 
 // T bf16 rows of K values in global memory (ld apart, 16-byte aligned) become operand rows in shared
-// memory (row_bytes(KT) apart), by all consumers: f16 times a power of two per row (exact for every
-// element within 2^28 of the row's largest; smaller ones are rounded to 2^-39 of it), columns from K
-// on zero. Only the 128-column groups for which used(group) holds are read and written. emax[t] (zero
-// before) receives the rows' largest exponent fields. Ends with a consumer barrier. A thread
+// memory (row_bytes(KT) apart), by all consumers: f16 times a power of two per row, columns from K
+// on zero. Only the 128-column groups for which used(group) holds are read and written. emax[t] and low[t] (0
+// and ~0 before) receive the rows' largest exponent fields and smallest magnitudes (low is free afterwards).
+// Returns whether a row's elements lie too far apart for that (wide_row; an element then loses bits, and is 0 more
+// than 2^39 below the largest); what needs those rows takes exact_dot instead. Ends with a consumer barrier. A thread
 // keeps up to kHeld chunks in registers between finding the maximum and converting; what lies beyond
 // is read again. requested: an
 // mbarrier that every consumer warp arrives at once its first loads are on the way.
 template <int kHeld, bool EvenFirst, class Used>
-__device__ __forceinline__ void convert_rows(const uint16_t *x, int64_t ld, uint8_t *rows, int T, int K, int KT,
-                                             uint32_t *emax, Used used, uint32_t requested = 0) {
+__device__ __forceinline__ bool convert_rows(const uint16_t *x, int64_t ld, uint8_t *rows, int T, int K, int KT,
+                                             uint32_t *emax, uint32_t *low, Used used, uint32_t requested = 0) {
     const int chunks = ((KT + 1) / 2) * 16;
     int tpr = kConsumerThreads;                              // threads per row, at least a warp
     while (tpr * T > kConsumerThreads) tpr >>= 1;
@@ -599,17 +618,30 @@ __device__ __forceinline__ void convert_rows(const uint16_t *x, int64_t ld, uint
     }
     if (requested && (threadIdx.x & 31) == 0) mbar_arrive_at(requested);
     if (t < T) {
-        uint32_t m = 0;
+        uint32_t m = 0, n = 0xFFFFFFFFu;
 #pragma unroll
         for (int j = 0; j < kHeld; ++j)
-            if (j < rounds) m = max_bits(v[j], m);
+            if (j < rounds) {
+                m = max_bits(v[j], m);
+                n = min_bits(v[j], n);
+            }
 #pragma unroll 4
         for (int i = i0 + kHeld * tpr; i * 8 < K; i += tpr)
-            if (used(i >> 4)) m = max_bits(row[i], m);
+            if (used(i >> 4)) {
+                const uint4 r = row[i];
+                m = max_bits(r, m);
+                n = min_bits(r, n);
+            }
         const uint32_t e = __reduce_max_sync(0xffffffffu, max(m >> 23, (m >> 7) & 0xFFu));
-        if ((threadIdx.x & 31) == 0) atomicMax(&emax[t], e);
+        const uint32_t l = __reduce_min_sync(0xffffffffu, min(n >> 16, n & 0xFFFFu));
+        if ((threadIdx.x & 31) == 0) {
+            atomicMax(&emax[t], e);
+            atomicMin(&low[t], l);
+        }
     }
     consumer_sync();
+    const int lane = threadIdx.x & 31;
+    const bool wide = __any_sync(0xffffffffu, lane < T && wide_row(emax[lane < T ? lane : 0], low[lane < T ? lane : 0]));
     if (t < T) {
         const float up = up_of(emax[t]);
         uint8_t *dst = rows + t * row_bytes(KT);
@@ -626,6 +658,46 @@ __device__ __forceinline__ void convert_rows(const uint16_t *x, int64_t ld, uint
                     i * 8 < K ? bf16x8_to_f16<EvenFirst>(row[i], up) : make_uint4(0, 0, 0, 0);
     }
     consumer_sync();
+    return wide;
+}
+
+// The sum of x w over the column tiles [ka, kb) of one row (of 128) of a row tile, from global memory in fp32 FMAs
+// (the products are exact): what takes the place of a piece's product where convert_rows finds rows too wide for f16.
+// Rarely needed (activations 2^31 and more apart in one row) and slow: 8 x 4096 x 32001 takes 304 us with it and 22
+// without, the decode layer of 8 tokens 282 and 44, the product of one token 1 x 2048 x 4096 16 and 8.
+template <bool EvenFirst>
+__device__ __forceinline__ float exact_dot(const uint8_t *codes, const uint8_t *scales, int ka, int kb, int row, const uint16_t *x, int K) {
+    float s = 0.f;
+#pragma unroll 1
+    for (int k = ka; k < kb; ++k) {
+        const uint8_t *ct = codes + (size_t)k * kTileCodeBytes + row * 16;
+        const uint32_t sc = *reinterpret_cast<const uint32_t *>(scales + (size_t)k * kTileScaleBytes + row * 4);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            const uint4 c4 = *reinterpret_cast<const uint4 *>(ct + h * (kTileCodeBytes / 2));
+            const uint32_t words[4] = {c4.x, c4.y, c4.z, c4.w}, two = e4m3x2_to_f16x2(sc >> (16 * h) & 0xFFFFu);
+            const __half2 m = *reinterpret_cast<const __half2 *>(&two);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const int col = k * kTileK + h * 32 + w * 8;
+                if (col >= K) break;                     // K is a multiple of 16: a chunk is inside or not
+                const uint4 xv = *reinterpret_cast<const uint4 *>(x + col);
+                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+                uint32_t f[4];
+                e2m1x8_to_f16x2x4(words[w], f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 wv = f16x2_to_float2(mul_f16x2(f[j], w < 2 ? __low2half2(m) : __high2half2(m)));
+                    // the pair's columns: 2j and 2j + 1, or with the even columns first 0 2, 4 6, 1 3, 5 7
+                    const uint32_t lo = EvenFirst ? xw[2 * (j & 1)] : xw[j], hi = EvenFirst ? xw[2 * (j & 1) + 1] : xw[j];
+                    const bool odd = EvenFirst && j >= 2;
+                    s = fmaf(bf16_bits_to_float(odd ? lo >> 16 : lo & 0xFFFFu), wv.x, s);
+                    s = fmaf(bf16_bits_to_float(odd || !EvenFirst ? hi >> 16 : hi & 0xFFFFu), wv.y, s);
+                }
+            }
+        }
+    }
+    return s;
 }
 
 }  // namespace stream
