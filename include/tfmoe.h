@@ -75,10 +75,11 @@ typedef struct tfmoe_layer tfmoe_layer;   /* opaque */
 #define TFMOE_FLAG_FORCE_GEMV    0x1u  /* every expert uses the CUDA-core GEMV regime */
 #define TFMOE_FLAG_FORCE_MMA     0x2u  /* every expert uses the tcgen05 tensor-core regime */
 #define TFMOE_FLAG_DEBUG_CHECKS  0x4u  /* kernels bounds-check ids/rows and set the error word */
-/* Test aid for the failure path: in every forward that runs the GEMV gate/up kernel,
- * one thread of its first CTA waits 1 ms on a barrier that nothing completes and then
- * takes the timeout path (error word, abort). That forward's output is undefined;
- * tfmoe_sync_status reports TFMOE_ERR_TIMEOUT. Not for production use. */
+/* Test aid for the failure path: in every forward that runs the GEMV gate/up kernel, in a
+ * handle's first tfmoe_forward_decode and in a tfmoe_linear's first forward, one thread of
+ * the first CTA waits 1 ms on a barrier that nothing completes and then
+ * takes the timeout path (error word, abort). That call's output is undefined;
+ * tfmoe_sync_status (tfmoe_linear_sync_status) reports TFMOE_ERR_TIMEOUT. Not for production use. */
 #define TFMOE_FLAG_TEST_TIMEOUT  0x8u
 
 /*
@@ -386,8 +387,8 @@ typedef enum {
 
 /*
  * in_features K: a positive multiple of 16, at most 65536; out_features N: 1 to 2^20;
- * max_tokens: 1 to 2^20, the largest T of a forward. flags: TFMOE_FLAG_OUT_FP32, and
- * TFMOE_FLAG_FORCE_GEMV (the streaming regime: up to 16 tokens, T * K up to about 64000) or
+ * max_tokens: 1 to 2^20, the largest T of a forward. flags: TFMOE_FLAG_OUT_FP32,
+ * TFMOE_FLAG_TEST_TIMEOUT, and TFMOE_FLAG_FORCE_GEMV (the streaming regime: up to 16 tokens, T * K up to about 64000) or
  * TFMOE_FLAG_FORCE_MMA (the tcgen05 regime at every T), which are exclusive.
  */
 typedef struct {

@@ -440,14 +440,19 @@ tfmoe_status tfmoe_sync_status(tfmoe_layer *layer, void *cuda_stream)
     if (!layer) return fail(TFMOE_ERR_INVALID_ARG, "tfmoe_sync_status: layer is NULL");
     Layer &L = layer->impl;
     DeviceGuard dg(L.device);
-    cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(cuda_stream));
+    const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    cudaError_t e = cudaStreamSynchronize(s);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "tfmoe_sync_status");
     int32_t word = 0;
     e = cudaMemcpy(&word, L.ws.err_word, sizeof word, cudaMemcpyDeviceToHost);
-    if (e == cudaSuccess && word != 0) e = cudaMemset(L.ws.err_word, 0, sizeof(int32_t));
-    if (e == cudaSuccess && (word & DEV_ERR_WAIT_TIMEOUT))
-        e = cudaMemset(L.ws.dec_arrivals, 0, decode_arrival_words() * sizeof(uint32_t));
+    if (e == cudaSuccess && word != 0) {
+        // done before this returns: the next forward may run on any stream
+        e = cudaMemsetAsync(L.ws.err_word, 0, sizeof(int32_t), s);
+        if (e == cudaSuccess && (word & DEV_ERR_WAIT_TIMEOUT))
+            e = cudaMemsetAsync(L.ws.dec_arrivals, 0, decode_arrival_words() * sizeof(uint32_t), s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "tfmoe_sync_status: error word");
     if (word & DEV_ERR_WAIT_TIMEOUT) return fail(TFMOE_ERR_TIMEOUT, "a device-side wait timed out (word 0x%x)", word);
     if (word) return fail(TFMOE_ERR_DEVICE, "device error word 0x%x (1 bad expert id, 2 bad row, 8 non-finite logit)", word);

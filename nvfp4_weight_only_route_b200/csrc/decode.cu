@@ -32,8 +32,9 @@
 // product runs on).
 //
 // The grid barriers need every CTA resident: a cooperative launch. Each wait is bounded; after a
-// timeout every CTA still arrives at every barrier, so that the arrival counters end where they
-// should, and the host's tfmoe_sync_status clears them.
+// timeout a CTA goes through the barriers without waiting, and CTA 0 may then set a counter back before the last
+// CTA has arrived at it. What is left in the counters is wrong until the host's tfmoe_sync_status
+// clears them with the error word (which ends the waits of the calls before that).
 #include <algorithm>
 
 #include "internal.h"
@@ -713,7 +714,8 @@ cudaError_t launch_decode(Layer &L, const uint16_t *x, int T, const uint16_t *re
     a.slots = decode_slots(L, T);
     a.row_area = decode_row_area(L, T);
     a.debug = (L.desc.flags & TFMOE_FLAG_DEBUG_CHECKS) ? 1 : 0;
-    a.test_wait_ns = (L.desc.flags & TFMOE_FLAG_TEST_TIMEOUT) ? kTestWaitNs : 0;
+    a.test_wait_ns = (L.desc.flags & TFMOE_FLAG_TEST_TIMEOUT) && !L.decode_timed_out ? kTestWaitNs : 0;
+    L.decode_timed_out = true;
     a.err_word = L.ws.err_word;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(L.num_sms);

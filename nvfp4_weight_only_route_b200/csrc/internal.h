@@ -138,6 +138,7 @@ struct Layer {
     bool prof_used[TFMOE_STAGE_COUNT] = {};
     float prof_ms[TFMOE_STAGE_COUNT] = {};
     int32_t prof_calls[TFMOE_STAGE_COUNT] = {};
+    bool decode_timed_out = false;  // TFMOE_FLAG_TEST_TIMEOUT: the first tfmoe_forward_decode has been
 };
 
 // Records the start/end events of one stage when profiling is on.

@@ -114,7 +114,7 @@ tfmoe_status tfmoe_linear_create(const tfmoe_linear_desc *desc, tfmoe_linear **o
         return record_error(TFMOE_ERR_INVALID_ARG, "unknown activation %d", d.activation);
     if ((d.flags & TFMOE_FLAG_FORCE_GEMV) && (d.flags & TFMOE_FLAG_FORCE_MMA))
         return record_error(TFMOE_ERR_INVALID_ARG, "FORCE_GEMV and FORCE_MMA are exclusive");
-    if (d.flags & ~(TFMOE_FLAG_FORCE_GEMV | TFMOE_FLAG_FORCE_MMA | TFMOE_FLAG_OUT_FP32))
+    if (d.flags & ~(TFMOE_FLAG_FORCE_GEMV | TFMOE_FLAG_FORCE_MMA | TFMOE_FLAG_OUT_FP32 | TFMOE_FLAG_TEST_TIMEOUT))
         return record_error(TFMOE_ERR_INVALID_ARG, "unknown flag bits 0x%x", d.flags);
     if (d.in_features > (1 << 16) || d.out_features > (1 << 20) || d.max_tokens > (1 << 20))
         return record_error(TFMOE_ERR_UNSUPPORTED, "tfmoe_linear supports in_features <= 65536, out_features <= 2^20 and "
@@ -127,6 +127,7 @@ tfmoe_status tfmoe_linear_create(const tfmoe_linear_desc *desc, tfmoe_linear **o
     if (!h) return record_error(TFMOE_ERR_OOM, "tfmoe_linear_create: host allocation failed");
     Linear &L = h->impl;
     L.desc = d;
+    L.test_timeout = (d.flags & TFMOE_FLAG_TEST_TIMEOUT) != 0;
     L.rows = linear_gated(L) ? 2 * d.out_features : d.out_features;
     L.RT = (L.rows + kTileRows - 1) / kTileRows;
     L.KT = (d.in_features + kTileK - 1) / kTileK;
@@ -245,6 +246,7 @@ tfmoe_status tfmoe_linear_forward(tfmoe_linear *lin, const uint16_t *x, int64_t 
     if (stream && !(L.desc.flags & TFMOE_FLAG_FORCE_GEMV)) stream = linear_stream_clocks(L, T) <= linear_tc_clocks(L, T);
     const cudaError_t e = stream ? launch_linear_stream(L, x, ldx, T, ep, s, &n) : launch_linear_tc(L, x, ldx, T, ep, s, &n);
     L.last_launches = n;
+    L.test_timeout = false;
     if (e != cudaSuccess) return cuda_fail(e, who);
     return record_ok();
 }
@@ -254,12 +256,17 @@ tfmoe_status tfmoe_linear_sync_status(tfmoe_linear *lin, void *cuda_stream)
     if (!lin) return record_error(TFMOE_ERR_INVALID_ARG, "tfmoe_linear_sync_status: lin is NULL");
     Linear &L = lin->impl;
     DeviceGuard dg(L.device);
-    cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(cuda_stream));
+    const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    cudaError_t e = cudaStreamSynchronize(s);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "tfmoe_linear_sync_status");
     int32_t word = 0;
     e = cudaMemcpy(&word, L.err_word, sizeof word, cudaMemcpyDeviceToHost);
-    if (e == cudaSuccess && word != 0) e = cudaMemset(L.ws_block, 0, L.zero_bytes);
+    if (e == cudaSuccess && word != 0) {
+        // done before this returns: the next forward may run on any stream
+        e = cudaMemsetAsync(L.ws_block, 0, L.zero_bytes, s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "tfmoe_linear_sync_status: error word");
     if (word) return record_error(TFMOE_ERR_TIMEOUT, "a device-side wait timed out (word 0x%x)", word);
     return record_ok();

@@ -38,7 +38,10 @@ struct Linear {
     size_t zero_bytes = 0;            // err_word and tickets, at the start of the workspace
     float *partial = nullptr;         // sums of cut row tiles
     int32_t last_launches = 0;
+    bool test_timeout = false;        // the next forward takes the timeout path (a test aid)
 };
+
+constexpr uint32_t kLinearTestWaitNs = 1000000;
 
 inline bool linear_gated(const Linear &L) { return L.desc.activation == TFMOE_ACT_SWIGLU; }
 

@@ -29,6 +29,7 @@ struct StreamArgs {
     float *partial;          // [2 G][T][128]: the first and the last piece of every CTA
     int32_t *tickets;        // [RT] arrivals per row tile, left at 0
     int32_t *err_word;
+    uint32_t test_wait_ns;   // > 0: CTA 0's producer waits that long for nothing and times out
     LinearEpilogue ep;
 };
 
@@ -120,6 +121,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
             Cursor cur;
             uint32_t issued = 0;
             bool ok = true;
+            if (a.test_wait_ns && c == 0) {                 // nobody else fills the first slot
+                const uint64_t t0 = global_timer_ns();
+                while (ok && !mbar_try_wait_sleep_at(ring.full, 0)) ok = global_timer_ns() - t0 <= a.test_wait_ns;
+                atomicOr(a.err_word, DEV_ERR_WAIT_TIMEOUT);
+                *ring.abort_flag = 1;
+            }
             // Two slots at once, the rest behind the requests for the token rows: rows queued behind
             // a whole ring of weights arrive 3 us later.
             auto rows_first = [&](uint32_t n) { if (n == 2) wait(ring, requested, 0); };
@@ -286,6 +293,7 @@ cudaError_t launch_linear_stream(Linear &L, const uint16_t *x, int64_t ldx, int 
     a.T = T; a.K = L.desc.in_features; a.RT = L.RT; a.KT = L.KT;
     a.slots = slots_for(T, L.KT);
     a.partial = L.partial; a.tickets = L.tickets; a.err_word = L.err_word;
+    a.test_wait_ns = L.test_timeout ? kLinearTestWaitNs : 0;
     a.ep = ep;
     const int grid = (int)std::min<int64_t>(L.num_sms, (int64_t)L.RT * L.KT);
     const size_t smem = Layout(T, L.KT, a.slots).total;

@@ -84,6 +84,7 @@ struct TcArgs {
     float *partial;                          // [items][N][128]
     int32_t *tickets;                        // [tiles], left at 0
     int32_t *err_word;
+    uint32_t test_wait_ns;                   // > 0: CTA 0's token copies wait that long for nothing and time out
     LinearEpilogue ep;
 };
 
@@ -299,6 +300,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             uint32_t issued = 0, ph = 0;
             int s = 0;
             bool ok = true;
+            if (a.test_wait_ns && tokens && blockIdx.x == 0) {       // nobody else fills the first stage
+                const uint64_t t0 = global_timer_ns();
+                while (ok && !mbar_try_wait_sleep(&full[0], 0)) ok = global_timer_ns() - t0 <= a.test_wait_ns;
+                atomicOr(err, DEV_ERR_WAIT_TIMEOUT);
+                *reinterpret_cast<volatile int32_t *>(&sm.abort_flag) = 1;
+            }
             for (int i = blockIdx.x; i < a.items && ok; i += gridDim.x) {
                 const Item it(a, i);
                 for (int kt = it.k0; kt < it.k1; kt += step) {
@@ -414,8 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 tmem_st16(col, r);
                 tmem_st16(col + 16u, r + 16);
                 ok = wait_warp(sm, &sm.bfull[s], ps, err);
+                tc_wait_st();                    // after an abort too: tensor memory is freed at the end
                 if (!ok) break;
-                tc_wait_st();
                 tc_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.ready[s]);
@@ -588,6 +595,7 @@ cudaError_t launch_linear_tc(Linear &L, const uint16_t *x, int64_t ldx, int T, c
     a.N = plan.N; a.splits = plan.splits;
     a.items = L.RT * ((T + plan.N - 1) / plan.N) * plan.splits;
     a.partial = L.partial; a.tickets = L.tickets; a.err_word = L.err_word;
+    a.test_wait_ns = L.test_timeout ? kLinearTestWaitNs : 0;
     a.ep = ep;
     CUtensorMap map;
     if (encode_tensor_map_2d(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, const_cast<uint16_t *>(x), (uint64_t)L.desc.in_features,
