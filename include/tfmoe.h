@@ -147,9 +147,12 @@ TFMOE_API tfmoe_status tfmoe_create(const tfmoe_layer_desc *desc, tfmoe_layer **
 
 /* Copy the caller's canonical weights into library-owned device memory,
  * repacked into the tiled kernel layout (row tiles of 128, K tiles of 64,
- * gate and up rows interleaved). Synchronous: returns after the copy is
+ * gate and up rows interleaved). Synchronous, after all work enqueued on the
+ * device before it (what writes the caller's tensors on any stream, forwards
+ * that read the old weights): returns after the copy is
  * complete; the caller may free its tensors afterwards. May be called again
- * to replace the weights. */
+ * to replace the weights. It synchronises the device, so not while a stream
+ * of the device is being captured. */
 TFMOE_API tfmoe_status tfmoe_load_weights(tfmoe_layer *layer, const tfmoe_weights *w);
 
 /*
@@ -416,8 +419,8 @@ typedef struct {
 TFMOE_API tfmoe_status tfmoe_linear_create(const tfmoe_linear_desc *desc, tfmoe_linear **out);
 
 /* Copy and repack the weights into library-owned memory (row tiles of 128, K tiles of 64, both
- * filled up with zeros). Synchronous, after all work enqueued on the device before it; may be
- * called again to replace the weights. */
+ * filled up with zeros). Synchronous, after all work enqueued on the device before it (so not while
+ * a stream of the device is being captured); may be called again to replace the weights. */
 TFMOE_API tfmoe_status tfmoe_linear_load_weights(tfmoe_linear *lin, const tfmoe_linear_weights *w);
 
 /*
