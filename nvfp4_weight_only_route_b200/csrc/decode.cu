@@ -18,14 +18,15 @@
 //   combine    out = bf16(sum_s g_s y_s + residual), slots in order, the tiles of 128 outputs spread over
 //              the SMs; with norm weights one CTA per token, which then has the row for its RMS norm
 //
-// The down run's first tiles are on chip before barrier 1 opens, so HBM idles only where a ring's
-// worth of bytes (about 180 KB per SM, 4 us) does not cover a barrier. All sums across CTAs are added
+// The down run's first tiles are on chip before barrier 1 opens: a ring's worth of bytes (10 slots, 184 KB per SM,
+// with one token; 8, 147 KB, with 8 tokens of H 2048; 4, 74 KB, with 14 of H 4096). All sums across CTAs are added
 // in a fixed order: equal calls give equal bits.
 //
-// Measured, calls in a row: H 2048, I 768, E 128, top 8 with one token 20.7 us, with 8 tokens 44.6 (137 MB: 3.1
-// TB/s over all, HBM's pace within the streams), with shared expert, residual and norm 52; H 4096, I 1536, 14 tokens
-// 176 (810 MB: 4.6 TB/s); H 4096, I 2688, E 256, one token 46 (151 MB: 3.3 TB/s). What bounds the small ones is the
-// latency of the phases between the streams: about 14 us with one token, 20 with 8.
+// Measured, calls in a row on rotating weights: H 2048, I 768, E 128, top 8 with one token 22.6 us, with 8 tokens 47
+// (137 MB: 2.9 TB/s over all), with shared expert, residual and norm 53; H 4096, I 1536, 14 tokens
+// 189 (810 MB: 4.3 TB/s); H 4096, I 2688, E 256, one token 48 (151 MB: 3.2 TB/s). By device timestamps (weights out of
+// L2, the slowest CTA) the gate/up stream of 8 tokens runs at 4.2 TB/s, that of the 14 at 5.5, of the large layer's one at
+// 4.3; outside the two streams are 7 us before them, 4 to 5 of barrier 1 and a rows and 4 of barrier 2 and combine with 8 tokens.
 //
 // a is rounded to f16 times a power of two per token and expert: 11 significant bits, exact
 // range within 2^-39 of the row's largest (8 times finer than bf16, at no cost: f16 is what the

@@ -7,8 +7,9 @@
 // leaves its pieces' sums in global memory (at most two pieces per CTA: its first and its last), and
 // the CTA that arrives last at the tile's counter adds them in CTA order and finishes it: no
 // CTA waits for another, so the launch needs no co-residency, and equal calls give equal bits.
-// Measured, calls in a row: 1 x 2048 x 4096 7.7 us, 8 x 4096 x 32001 with fp32 out 21.2 (75 MB: 3.5 TB/s over all); a
-// start of 7 us (one row) to 12 (16 rows), and 0.42 to 0.65 us per window of 18.4 KB and SM (HBM's pace is 0.42).
+// Measured, calls in a row on rotating weights: 1 x 2048 x 4096 8.3 us, 8 x 4096 x 32001 with fp32 out 22.7 (75 MB: 3.3 TB/s
+// over all). Fitted to calls on one matrix, which L2 may hold: a start of 7 us (one row) to 12 (16 rows), and 0.42 to
+// 0.65 us per window of 18.4 KB and SM (HBM's pace is 0.42).
 // The launch is a programmatic dependent of the one before it: the weights, which no kernel
 // writes, start to stream before that kernel has ended.
 #include <algorithm>
@@ -266,7 +267,7 @@ bool linear_stream_fits(const Linear &L, int T) { return T <= kMaxTokens && slot
 // The estimated time of a call in clocks of an SM, to set beside the tcgen05 regime's: a start (token rows,
 // first weights, joined tiles) that grows with the rows, and the SM's windows of the weight stream. Fitted to
 // launches of 1 to 16 tokens over 12 matrices. With few windows and many rows tcgen05 wins (16 x 4096 x 2 x 2688:
-// 10.9 us against 15.6), with many windows this regime (8 x 4096 x 32001: 21.2 us against 33.3).
+// 10.9 us against 15.6), with many windows this regime (8 x 4096 x 32001: 22.7 us against 33.3).
 double linear_stream_clocks(const Linear &L, int T) {
     const double windows = (double)L.RT * L.KT / L.num_sms / kWindow;
     return T <= 8 ? 13000.0 + 520.0 * (T - 1) + 830.0 * windows : 21500.0 + 190.0 * (T - 9) + 1250.0 * windows;

@@ -236,7 +236,8 @@ struct Lane {
 // is converted, across windows and pieces, and a slot is handed back when the last of it is read.
 //
 // WindowConsumer: a group takes both pairs of every second window: one wait, one hand-back and one set of
-// counters for two pairs (0.42 us per window and SM, HBM's pace, against 0.48 with one token row). The ring has an
+// counters for two pairs (0.42 us per window and SM against 0.48 with one token row, on weights that L2 holds; HBM's
+// pace is 0.42). The ring has an
 // even number of slots, so that a group's windows are all the phases of every second slot, in order: a
 // group that saw only some phases of a slot could take an older phase's parity for the one it waits for.
 template <int NT>

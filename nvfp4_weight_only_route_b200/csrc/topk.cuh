@@ -26,14 +26,14 @@ __device__ __forceinline__ float logit_of_key(uint32_t k) {
 // weight over the k selected logits. Each lane keeps its best remaining expert (largest key, lower
 // expert on ties); a round takes the warp's largest key and the lowest expert that holds it (two
 // redux.sync), so ties go to the lower expert index, and only the winner's lane searches its next best.
-template <int kMaxEPerLane>
+template <int kPerLane>
 __device__ __forceinline__ void topk_lanes(const float *row, int E, int k, int &my_id, float &my_w)
 {
     const int lane = threadIdx.x & 31;
-    uint32_t key[kMaxEPerLane];
+    uint32_t key[kPerLane];
     uint32_t left = 0;                        // bit i: candidate lane + 32 i remains
 #pragma unroll
-    for (int i = 0; i < kMaxEPerLane; ++i) {
+    for (int i = 0; i < kPerLane; ++i) {
         const int e = lane + 32 * i;
         const bool in = e < E;
         key[i] = in ? logit_key(__ldcg(row + e)) : 0u;
@@ -44,7 +44,7 @@ __device__ __forceinline__ void topk_lanes(const float *row, int E, int k, int &
         best_key = 0u;
         best_id = 0xffffffffu;
 #pragma unroll
-        for (int i = kMaxEPerLane - 1; i >= 0; --i)       // downwards: the lower expert keeps ties
+        for (int i = kPerLane - 1; i >= 0; --i)           // downwards: the lower expert keeps ties
             if ((left & (1u << i)) && key[i] >= best_key) {
                 best_key = key[i];
                 best_id = (uint32_t)(lane + 32 * i);
