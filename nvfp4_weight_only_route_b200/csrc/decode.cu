@@ -451,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeArgs a)
     ring.empty = ring.full + 8u * kMaxSlots;
     ring.zeros = smem_u32(smem + lay.zeros);
     ring.n = a.slots;
+    ring.early = false;
     ring.abort_flag = reinterpret_cast<volatile int32_t *>(bars + 2 * kMaxSlots + 2);
     ring.err_word = a.err_word;
     const uint32_t planned = ring.full + 8u * (2 * kMaxSlots);

@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
     ring.empty = ring.full + 8u * kMaxSlots;
     ring.zeros = smem_u32(smem + lay.zeros);
     ring.n = a.slots;
+    ring.early = true;
     ring.abort_flag = reinterpret_cast<volatile int32_t *>(bars + 2 * kMaxSlots + 1);
     const uint32_t requested = ring.full + 8u * (2 * kMaxSlots);
     ring.err_word = a.err_word;

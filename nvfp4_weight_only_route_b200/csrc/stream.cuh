@@ -83,19 +83,29 @@ struct Ring {
     uint32_t slots, full, empty;          // shared addresses
     uint32_t zeros;                       // shared address of 256 zero bytes
     int n;                                // slots in use
+    bool early;                           // the kernel may have started before the one ahead of it has ended
     volatile int32_t *abort_flag;         // shared
     int32_t *err_word;                    // global
 };
 
-// Bounded wait: false once another thread has given up or after kWaitLimitNs (recorded).
+// Bounded wait: false once another thread has given up or after kWaitLimitNs (recorded). In a kernel that started
+// early the time of the kernel ahead does not count: when the limit passes, that one is waited for and the
+// clock set back, once.
 __device__ __forceinline__ bool wait(const Ring &r, uint32_t bar, uint32_t parity) {
     if (mbar_try_wait_at(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
+    uint64_t t0 = global_timer_ns();
+    bool again = r.early;
     while (true) {
         for (int i = 0; i < 4; ++i)
             if (mbar_try_wait_sleep_at(bar, parity)) return true;
         if (*r.abort_flag) return false;
         if (global_timer_ns() - t0 > kWaitLimitNs) {
+            if (again) {
+                again = false;
+                grid_dep_wait();
+                t0 = global_timer_ns();
+                continue;
+            }
             atomicOr(r.err_word, DEV_ERR_WAIT_TIMEOUT);
             *r.abort_flag = 1;
             return false;
