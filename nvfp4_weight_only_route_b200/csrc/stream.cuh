@@ -61,7 +61,7 @@ __host__ __device__ constexpr uint32_t chunk_offset(int k) {
 }
 
 // U units cut into G runs: the first unit of run c, and the run that holds unit u. The handles keep
-// U below 2^24 and G is at most the SM count, so the products fit 32 bits. A quotient below G is
+// U at 2^24 or less (256 experts of 16384 x 16384) and G is at most the SM count, so the products fit 32 bits. A quotient below G is
 // found by one multiplication with the reciprocal (relative error below 2^-22) and a correction.
 struct Runs {
     uint32_t U, G;
