@@ -374,11 +374,11 @@ class Linear:
         import torch
         K, N = self._widths
         gated = self.desc.activation == ACTIVATIONS.index("swiglu")
-        bytes_, fp32 = (torch.uint8, torch.int8), (torch.float32,)
-        scales = bytes_ + (torch.float8_e4m3fn,)
+        fp32 = (torch.float32,)
+        codes, scales = (torch.uint8, torch.int8, torch.float4_e2m1fn_x2), (torch.uint8, torch.int8, torch.float8_e4m3fn)
         read = {}
         for p in ("", "up_") if gated else ("",):
-            read.update({p + "codes": (N, K // 2, bytes_), p + "scales": (N, K // 16, scales), p + "global": (1, 1, fp32)})
+            read.update({p + "codes": (N, K // 2, codes), p + "scales": (N, K // 16, scales), p + "global": (1, 1, fp32)})
         if self.desc.has_bias:
             read["bias"] = (1, 2 * N if gated else N, fp32)
         for name, (rows, width, dtypes) in read.items():

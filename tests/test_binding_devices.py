@@ -146,6 +146,9 @@ def test_load_weights_of_the_product_takes_what_it_reads():
     plain = _linear()
     plain.load_weights(w)
     assert [n for n, _ in lin.lib.calls + plain.lib.calls] == ["tfmoe_linear_load_weights"] * 2
+    packed = _linear()                                                  # the bytes by their types' names
+    packed.load_weights({**_weights(), "codes": FakeTensor((48, 32), "cuda:0", torch.float4_e2m1fn_x2)})
+    assert len(packed.lib.calls) == 1
     given = plain.lib.calls[0][1][1]._obj
     assert given.codes == 4096 and given.bias is None and given.up_codes is None
     missing = _linear()
